@@ -27,6 +27,8 @@ __all__ = [
     "fp8_quant_group_float", "fp8_block_quant_128x128_float", "fp8_block_gemm_nt_float_scales",
     "fp8_weight_preshuffle", "fp8_block_gemm_nt_preshuffled", "fp8_block_gemm_grouped_masked_preshuffled",
     "fp8_block_gemm_nt_preshuffled_noalloc", "check_dense_shapes", "check_masked_shapes", "check_contiguous_shapes",
+    "moe_route_topk", "moe_route_topk_backward", "moe_combine", "moe_combine_backward", "residual_rms_norm",
+    "residual_rms_norm_backward", "silu_mul_quant_group_pack_checkpoint", "silu_mul_backward_from_checkpoint",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +44,7 @@ _lib = ctypes.CDLL(_LIB_PATH)
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F32 = ctypes.c_float
 _I32P = ctypes.POINTER(ctypes.c_int32)
 
 _SIGS = {
@@ -69,6 +72,16 @@ _SIGS = {
     "fp8_block_gemm_grouped_contiguous": [_P, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _P],
     "fp8_block_gemm_grouped_contiguous_cfg": [_P, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I32,
                                               _P],
+    "moe_route_topk": [_P, _I32, _I64, _I64, _I64, _P, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P, _P, _P],
+    "moe_route_topk_backward": [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32, _I32, _F32, _P, _I64, _P],
+    "moe_combine": [_P, _P, _P, _P, _P, _I64, _I64, _I32, _I64, _I64, _I64, _P, _I64, _P],
+    "moe_combine_backward": [_P, _I64, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P],
+    "residual_rms_norm": [_P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _F32, _F32, _F32, _I64, _I64, _P, _I64, _P, _I64,
+                          _P, _I64, _P, _I64, _P],
+    "residual_rms_norm_backward": [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _F32, _F32, _F32,
+                                   _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P],
+    "silu_mul_quant_group_pack_checkpoint": [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P],
+    "silu_mul_backward_from_checkpoint": [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P],
     "fp8bs_gemm_config_count": [],
     "fp8bs_gemm_config": [ctypes.c_int, _I64, _I64, _I64, _I32P, _I32P, _I32P, _I32P],
     "fp8bs_gemm_config_of": [_I32, ctypes.c_int, _I64, _I64, _I64, _I32, _I32P, _I32P, _I32P],
@@ -618,3 +631,9 @@ def gemm_config(masked, M: int, N: int, K: int) -> dict:
                                 ctypes.byref(bn), ctypes.byref(sp))
     _check("fp8bs_gemm_config", st)
     return {"kernel": k.value, "bm": bm.value, "bn": bn.value, "splits": sp.value}
+
+
+# the operators around the experts' products bind the same library
+from .block_ops import (  # noqa: E402
+    moe_combine, moe_combine_backward, moe_route_topk, moe_route_topk_backward, residual_rms_norm,
+    residual_rms_norm_backward, silu_mul_backward_from_checkpoint, silu_mul_quant_group_pack_checkpoint)

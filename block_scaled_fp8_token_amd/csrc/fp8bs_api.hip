@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/fp8bs.h"
+#include "block_launch.hpp"
 #include "fp8bs_launch.hpp"
 
 namespace {
@@ -250,6 +251,81 @@ fp8bs::GemmProblem host_problem(int layout, int64_t M, int64_t N, int64_t K) {
   p.float_scales = layout == 3 || layout == 6;
   p.b_shuffled = layout == 4 || layout == 6;
   return p;
+}
+
+// Pointers and row strides of the operators around the experts' products.  A row of
+// bf16 or fp32 values is read and written 16 bytes at a time.
+bool aligned_or_null(const void* p, uintptr_t a) { return p == nullptr || aligned(p, a); }
+bool bad_rows(const void* p, int64_t ld, int64_t N) { return p != nullptr && ld < N; }
+bool misaligned_rows(const void* p, int64_t ld) { return p != nullptr && (!aligned(p, 16) || ld % 8 != 0); }
+
+int check_route(int64_t ld, int64_t T, int64_t E, int32_t logits_f32, int32_t scoring, int32_t topk) {
+  if (T < 0 || E < 1 || E > fp8bs::kRouteMaxE || ld < E || T > 4 * (int64_t)INT32_MAX) return FP8BS_ERR_SHAPE;
+  if (topk < 1 || topk > fp8bs::kRouteMaxTopk || topk > E) return FP8BS_ERR_SHAPE;
+  if ((logits_f32 != 0 && logits_f32 != 1) || (scoring != FP8BS_SIGMOID && scoring != FP8BS_SOFTMAX))
+    return FP8BS_ERR_SHAPE;
+  return FP8BS_OK;
+}
+
+fp8bs::RouteProblem route_problem(const void* logits, int32_t logits_f32, int64_t ld, int64_t T, int64_t E,
+                                  int32_t scoring, int32_t topk, int32_t renormalize, float scale) {
+  fp8bs::RouteProblem p;
+  p.logits = logits;
+  p.f32 = logits_f32 != 0;
+  p.ld = ld;
+  p.T = T;
+  p.E = (int)E;
+  p.topk = topk;
+  p.softmax = scoring == FP8BS_SOFTMAX;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  return p;
+}
+
+// Sizes of the combine and its backward pass; 1: nothing to do.
+int check_combine(int64_t T, int32_t topk, int64_t E, int64_t M_max, int64_t N) {
+  if (T < 0 || E < 0 || M_max < 0 || N < 0 || N % 8 != 0 || topk < 1 || topk > 64) return FP8BS_ERR_SHAPE;
+  if (T > INT32_MAX || E > INT32_MAX || M_max > INT32_MAX || T * ((N + 2047) / 2048) > INT32_MAX)
+    return FP8BS_ERR_SHAPE;
+  return T == 0 || N == 0 ? 1 : FP8BS_OK;
+}
+
+// Arguments that the norm and its backward pass share.
+int check_norm(int32_t residual_f32, const void* y, int64_t ldy, const void* w_post, const void* gate, int64_t ld_gate,
+               const void* w_pre, int64_t T, int64_t N) {
+  if (T < 0 || N < 0 || N % 8 != 0 || N > fp8bs::kNormMaxN || (residual_f32 != 0 && residual_f32 != 1))
+    return FP8BS_ERR_SHAPE;
+  if (N == 0) return 1;
+  if (!w_pre || ((w_post || gate) && !y)) return FP8BS_ERR_NULL;
+  if (bad_rows(y, ldy, N) || (gate && ld_gate != 0 && ld_gate < N)) return FP8BS_ERR_SHAPE;
+  if (misaligned_rows(y, ldy) || misaligned_rows(gate, ld_gate) || !aligned(w_pre, 16) || !aligned_or_null(w_post, 16))
+    return FP8BS_ERR_ALIGN;
+  return FP8BS_OK;
+}
+
+fp8bs::NormProblem norm_problem(int32_t residual_f32, const void* y, int64_t ldy, const void* w_post, const void* gate,
+                                int64_t ld_gate, const void* w_pre, float residual_scale, float eps, float offset,
+                                int64_t T, int64_t N) {
+  fp8bs::NormProblem p;
+  p.f32 = residual_f32 != 0;
+  p.T = T;
+  p.N = N;
+  p.y = static_cast<const uint16_t*>(y);
+  p.ldy = ldy;
+  p.w_post = static_cast<const uint16_t*>(w_post);
+  p.gate = static_cast<const uint16_t*>(gate);
+  p.ld_gate = ld_gate;
+  p.w_pre = static_cast<const uint16_t*>(w_pre);
+  p.residual_scale = residual_scale;
+  p.eps = eps;
+  p.offset = offset;
+  return p;
+}
+
+int check_checkpoint(int64_t E, int64_t M_max, int64_t H) {
+  if (E < 0 || E > fp8bs::kCheckpointMaxE || M_max < 0 || H < 0 || H % 128 != 0) return FP8BS_ERR_SHAPE;
+  if (E * M_max > INT32_MAX || M_max > INT32_MAX || H > INT32_MAX) return FP8BS_ERR_SHAPE;
+  return E == 0 || M_max == 0 || H == 0 ? 1 : FP8BS_OK;
 }
 
 }  // namespace
@@ -569,6 +645,189 @@ int fp8_block_gemm_nt_float_scales_preshuffled_cfg(const void* a, const float* s
   fp8bs::GemmConfig cfg;
   if (!fp8bs::gemm_config_by_index(kernel, p, splits < 1 ? 1 : splits, &cfg)) return FP8BS_ERR_SHAPE;
   return run_gemm(p, cfg, static_cast<hipStream_t>(stream));
+}
+
+int moe_route_topk(const void* logits, int32_t logits_f32, int64_t ld, int64_t T, int64_t E, const float* bias,
+                   int32_t scoring, int32_t groups, int32_t topk_groups, int32_t group_top, int32_t topk,
+                   int32_t renormalize, float scale, int32_t* topk_ids, float* weights, void* stream) {
+  int st = check_route(ld, T, E, logits_f32, scoring, topk);
+  if (st != FP8BS_OK) return st;
+  if (groups < 1 || groups > 64 || E % groups != 0 || topk_groups < 1 || topk_groups > groups) return FP8BS_ERR_SHAPE;
+  if (topk > topk_groups * (E / groups) || group_top < 1 || group_top > 2 || group_top > E / groups)
+    return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!logits || !topk_ids || !weights) return FP8BS_ERR_NULL;
+  if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned_or_null(bias, 4) || !aligned(topk_ids, 4) ||
+      !aligned(weights, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::RouteProblem p = route_problem(logits, logits_f32, ld, T, E, scoring, topk, renormalize, scale);
+  hipError_t e = fp8bs::launch_route(p, bias, groups, topk_groups, group_top, topk_ids, weights,
+                                     static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int moe_route_topk_backward(const void* logits, int32_t logits_f32, int64_t ld, int64_t T, int64_t E,
+                            const int32_t* topk_ids, const float* d_weights, int32_t scoring, int32_t topk,
+                            int32_t renormalize, float scale, void* d_logits, int64_t ld_d, void* stream) {
+  int st = check_route(ld, T, E, logits_f32, scoring, topk);
+  if (st != FP8BS_OK) return st;
+  if (ld_d < E) return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!logits || !topk_ids || !d_weights || !d_logits) return FP8BS_ERR_NULL;
+  if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(d_logits, logits_f32 ? 4 : 2) || !aligned(topk_ids, 4) ||
+      !aligned(d_weights, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::RouteProblem p = route_problem(logits, logits_f32, ld, T, E, scoring, topk, renormalize, scale);
+  hipError_t e =
+      fp8bs::launch_route_backward(p, topk_ids, d_weights, d_logits, ld_d, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int moe_combine(const void* y, const int32_t* topk_ids, const int32_t* slot_of, const float* weights, const void* base,
+                int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t M_max, int64_t N, void* out,
+                int64_t ld_out, void* stream) {
+  int st = check_combine(T, topk, E, M_max, N);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (!topk_ids || !slot_of || !out || (!y && E > 0 && M_max > 0)) return FP8BS_ERR_NULL;
+  if (bad_rows(base, ld_base, N) || ld_out < N) return FP8BS_ERR_SHAPE;
+  if (!aligned_or_null(y, 16) || misaligned_rows(base, ld_base) || misaligned_rows(out, ld_out) ||
+      !aligned(topk_ids, 4) || !aligned(slot_of, 4) || !aligned_or_null(weights, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::CombineProblem p = {topk_ids, slot_of, weights, T, E, M_max, N, topk};
+  hipError_t e = fp8bs::launch_combine(p, static_cast<const uint16_t*>(y), static_cast<const uint16_t*>(base), ld_base,
+                                       static_cast<uint16_t*>(out), ld_out, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int moe_combine_backward(const void* d_out, int64_t ld_d, const void* y, const int32_t* topk_ids,
+                         const int32_t* slot_of, const float* weights, int64_t T, int32_t topk, int64_t E,
+                         int64_t M_max, int64_t N, void* d_y, void* q, uint32_t* sf, float* d_weights, void* stream) {
+  int st = check_combine(T, topk, E, M_max, N);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  const bool rows = E > 0 && M_max > 0;  // a layout without rows has no pointers
+  if (!d_out || !topk_ids || !slot_of || (rows && (!d_y == !q || !q != !sf || (d_weights && !y)))) return FP8BS_ERR_NULL;
+  if (ld_d < N || (q && N % 128 != 0)) return FP8BS_ERR_SHAPE;
+  if (misaligned_rows(d_out, ld_d) || !aligned_or_null(y, 16) || !aligned_or_null(d_y, 16) || !aligned_or_null(q, 16) ||
+      !aligned_or_null(sf, 4) || !aligned(topk_ids, 4) || !aligned(slot_of, 4) || !aligned_or_null(weights, 4) ||
+      !aligned_or_null(d_weights, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::CombineProblem p = {topk_ids, slot_of, weights, T, E, M_max, N, topk};
+  hipError_t e = fp8bs::launch_combine_backward(p, static_cast<const uint16_t*>(d_out), ld_d,
+                                                static_cast<const uint16_t*>(y), static_cast<uint16_t*>(d_y),
+                                                static_cast<uint8_t*>(q), sf, d_weights,
+                                                static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int residual_rms_norm(const void* x, int64_t ldx, int32_t residual_f32, const void* y, int64_t ldy, const void* w_post,
+                      const void* gate, int64_t ld_gate, const void* w_pre, float residual_scale, float eps,
+                      float weight_offset, int64_t T, int64_t N, void* h, int64_t ldh, void* z, int64_t ldz, void* q,
+                      int64_t ldq, uint32_t* sf, int64_t ld_sf, void* stream) {
+  if (T == 0 && N >= 0) y = w_post = gate = nullptr;  // no rows: their pointers are not looked at
+  int st = check_norm(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, T, N);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (q && N % 128 != 0) return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!x || !q != !sf || (!h && !z && !q)) return FP8BS_ERR_NULL;
+  if (ldx < N || bad_rows(h, ldh, N) || bad_rows(z, ldz, N) || bad_rows(q, ldq, N) || (sf && ld_sf < T))
+    return FP8BS_ERR_SHAPE;
+  if (misaligned_rows(x, ldx) || misaligned_rows(h, ldh) || misaligned_rows(z, ldz) || misaligned_rows(q, ldq) ||
+      (q && ldq % 16 != 0) || !aligned_or_null(sf, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::NormProblem p = norm_problem(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, residual_scale, eps,
+                                            weight_offset, T, N);
+  hipError_t e = fp8bs::launch_norm(p, x, ldx, h, ldh, static_cast<uint16_t*>(z), ldz, static_cast<uint8_t*>(q), ldq,
+                                    sf, ld_sf, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, int64_t ld_dh, const void* h,
+                               int64_t ldh, int32_t residual_f32, const void* y, int64_t ldy, const void* w_post,
+                               const void* gate, int64_t ld_gate, const void* w_pre, float residual_scale, float eps,
+                               float weight_offset, int64_t T, int64_t N, void* d_x, int64_t ld_dx, void* d_y,
+                               int64_t ld_dy, float* d_w_pre, float* d_w_post, void* d_gate, int64_t ld_dgate,
+                               void* stream) {
+  if (T < 0 || N < 0 || N % 8 != 0 || N > fp8bs::kNormMaxN) return FP8BS_ERR_SHAPE;
+  if (T == 0) {
+    if (N == 0) return FP8BS_OK;
+    if (!d_w_pre) return FP8BS_ERR_NULL;
+    int st = check_device();
+    if (st != FP8BS_OK) return st;
+    float* sums[3] = {d_w_pre, d_w_post, ld_gate == 0 ? static_cast<float*>(d_gate) : nullptr};
+    for (float* s : sums) {
+      if (s == nullptr) continue;
+      hipError_t e = zero_words(s, (size_t)N * sizeof(float), static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return fail_hip(e);
+    }
+    return FP8BS_OK;
+  }
+  int st = check_norm(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, T, N);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (!d_z || !h || !d_x || !d_w_pre || !y != !d_y || !w_post != !d_w_post || !gate != !d_gate) return FP8BS_ERR_NULL;
+  if (ld_dz < N || bad_rows(d_h, ld_dh, N) || ldh < N || ld_dx < N || bad_rows(d_y, ld_dy, N) ||
+      (gate && ld_gate != 0 && ld_dgate < N))
+    return FP8BS_ERR_SHAPE;
+  if (misaligned_rows(d_z, ld_dz) || misaligned_rows(d_h, ld_dh) || misaligned_rows(h, ldh) ||
+      misaligned_rows(d_x, ld_dx) || misaligned_rows(d_y, ld_dy) || !aligned(d_w_pre, 16) ||
+      !aligned_or_null(d_w_post, 16) || !aligned_or_null(d_gate, 16) || (gate && ld_gate != 0 && ld_dgate % 8 != 0))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::NormProblem p = norm_problem(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, residual_scale, eps,
+                                            weight_offset, T, N);
+  const fp8bs::NormGradients g = {static_cast<const uint16_t*>(d_z), ld_dz, d_h, ld_dh, h, ldh, d_x, ld_dx,
+                                  static_cast<uint16_t*>(d_y), ld_dy, d_w_pre, d_w_post, d_gate, ld_dgate};
+  // partial sums live in the stream's workspace past the split-K arrival counters
+  const size_t off = fp8bs::gemm_workspace_zeroed_prefix();
+  void* ws = nullptr;
+  st = get_workspace(off + fp8bs::norm_backward_scratch_bytes(p, g), static_cast<hipStream_t>(stream), &ws);
+  if (st != FP8BS_OK) return st;
+  hipError_t e = fp8bs::launch_norm_backward(p, g, reinterpret_cast<float*>(static_cast<char*>(ws) + off),
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int silu_mul_quant_group_pack_checkpoint(const void* x, const int32_t* masked_m, int64_t E, int64_t M_max, int64_t H,
+                                         void* q, uint32_t* sf, void* cq, uint32_t* csf, void* stream) {
+  int st = check_checkpoint(E, M_max, H);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (!x || !masked_m || !q || !sf || !cq || !csf) return FP8BS_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(cq, 16) || !aligned(sf, 4) || !aligned(csf, 4) ||
+      !aligned(masked_m, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  hipError_t e = fp8bs::launch_silu_checkpoint(static_cast<const uint16_t*>(x), masked_m, E, M_max, H,
+                                               static_cast<uint8_t*>(q), sf, static_cast<uint8_t*>(cq), csf,
+                                               static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int silu_mul_backward_from_checkpoint(const void* d_y, const int32_t* masked_m, int64_t E, int64_t M_max, int64_t H,
+                                      const void* cq, const uint32_t* csf, void* d_x, void* q, uint32_t* sf,
+                                      void* stream) {
+  int st = check_checkpoint(E, M_max, H);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (!d_y || !masked_m || !cq || !csf || !d_x == !q || !q != !sf) return FP8BS_ERR_NULL;
+  if (!aligned(d_y, 16) || !aligned(cq, 16) || !aligned_or_null(d_x, 16) || !aligned_or_null(q, 16) ||
+      !aligned(csf, 4) || !aligned_or_null(sf, 4) || !aligned(masked_m, 4))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  hipError_t e = fp8bs::launch_silu_backward(static_cast<const uint16_t*>(d_y), masked_m, E, M_max, H,
+                                             static_cast<const uint8_t*>(cq), csf, static_cast<uint16_t*>(d_x),
+                                             static_cast<uint8_t*>(q), sf, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
 }
 
 int fp8bs_gemm_config_count(void) { return fp8bs::gemm_config_count(); }

@@ -330,6 +330,115 @@ int fp8_block_gemm_grouped_masked_preshuffled_cfg(const void* a, const uint32_t*
                                                   int64_t E, int64_t M_max, int64_t N, int64_t K,
                                                   int32_t kernel, void* stream);
 
+/*
+ * The operators around the experts' products: routing, combine, the norms of the
+ * residual stream, and an 8-bit checkpoint of the gated activation, each with its
+ * backward pass.  The conventions at the top of this file hold; rows that a call
+ * leaves out (padding, pairs without a slot) are neither read nor written.
+ */
+enum { FP8BS_SIGMOID = 0, FP8BS_SOFTMAX = 1 };
+
+/*
+ * Routing.  For the logits l of a token over E experts:
+ *   scores s = sigmoid(l) or softmax(l) (scoring);
+ *   ranks  r = s + bias if bias is given, else l;
+ *   groups of E / groups consecutive experts are scored by their best rank
+ *   (group_top = 1) or by the sum of the two best (group_top = 2; without a bias the sum
+ *   of the two best s); the topk_groups best groups take part, ties to the lowest group;
+ *   the topk best ranks in them are chosen in descending order, ties to the lowest expert;
+ *   weights w = scale * s, divided by the sum of the chosen s if renormalize is not 0
+ *   (0 where that sum is 0; the softmax's is formed over the chosen logits).
+ * An expert whose logit is NaN or -infinity, or whose rank is (a NaN bias), is not
+ * available; where fewer than topk are, the ids that are left are -1 with weight 0, which
+ * every other entry point takes as a pair that goes nowhere.  +infinity counts as the
+ * largest finite logit.  All arithmetic is fp32.
+ *   logits   : fp32 (logits_f32 = 1) or bf16 [T][ld], ld >= E; aligned to their type only
+ *   bias     : fp32 [E] or NULL
+ *   topk_ids : int32 [T][topk] out;  weights : fp32 [T][topk] out
+ *   1 <= E <= 1024, 1 <= topk <= 64, groups divides E, groups <= 64,
+ *   1 <= topk_groups <= groups, topk <= topk_groups * E / groups, group_top <= E / groups.
+ * Backward: the choice is held fixed and the bias gets no gradient.  d_logits [T][ld_d]
+ * has the type of the logits and is written whole, zeros included.  logits, topk_ids and
+ * the options are the forward's; an id of -1 takes no part.
+ */
+int moe_route_topk(const void* logits, int32_t logits_f32, int64_t ld, int64_t T, int64_t E, const float* bias,
+                   int32_t scoring, int32_t groups, int32_t topk_groups, int32_t group_top, int32_t topk,
+                   int32_t renormalize, float scale, int32_t* topk_ids, float* weights, void* stream);
+int moe_route_topk_backward(const void* logits, int32_t logits_f32, int64_t ld, int64_t T, int64_t E,
+                            const int32_t* topk_ids, const float* d_weights, int32_t scoring, int32_t topk,
+                            int32_t renormalize, float scale, void* d_logits, int64_t ld_d, void* stream);
+
+/*
+ * Combine: the experts' rows back to their tokens.
+ *   out[t] = base[t] + sum_j weights[t][j] * y[topk_ids[t][j]][slot_of[t][j]]
+ * in fp32, j ascending, rounded once.  A pair whose id is outside [0, E) or whose slot is
+ * outside [0, M_max) is left out.  With weights = NULL (ones) this is also the gradient of
+ * fp8_quant_group_pack_to_experts' dispatch.
+ *   y         : bf16 [E][M_max][N] (what the masked GEMM wrote)
+ *   topk_ids, slot_of : int32 [T][topk];  weights : fp32 [T][topk] or NULL
+ *   base      : bf16 [T][ld_base] or NULL;  out : bf16 [T][ld_out]
+ *   N % 8 == 0, 1 <= topk <= 64, ld_base and ld_out >= N and % 8 == 0.
+ * Backward, for every pair that has a row: d_y[e][s] = weights[t][j] * d_out[t], in bf16
+ * (d_y [E][M_max][N]) or, with d_y = NULL, as q e4m3 [E][M_max][N] and sf uint32
+ * [E][ceil(N/512)][M_max] quantized as fp8_quant_group_pack quantizes the fp32 values
+ * (N % 128 == 0), ready for the masked GEMM that takes the gradient on; and d_weights[t][j] =
+ * <d_out[t], y[e][s]> (0 for a pair without a row; NULL: not wanted, and y is not read).
+ * No two pairs may name the same row.
+ */
+int moe_combine(const void* y, const int32_t* topk_ids, const int32_t* slot_of, const float* weights, const void* base,
+                int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t M_max, int64_t N, void* out,
+                int64_t ld_out, void* stream);
+int moe_combine_backward(const void* d_out, int64_t ld_d, const void* y, const int32_t* topk_ids,
+                         const int32_t* slot_of, const float* weights, int64_t T, int32_t topk, int64_t E,
+                         int64_t M_max, int64_t N, void* d_y, void* q, uint32_t* sf, float* d_weights, void* stream);
+
+/*
+ * Norms before and after a block, with the block's gate and the residual's scale:
+ *   b = y * rsqrt(mean(y^2) + eps) * (w_post + weight_offset)    (b = y if w_post is NULL)
+ *   h = residual_scale * x + gate * b                            (no gate: 1; y NULL: b = 0)
+ *   z = h * rsqrt(mean(h^2) + eps) * (w_pre + weight_offset)
+ * in fp32; z comes from the unrounded h.  Any of h, z and (q, sf) may be NULL.
+ *   x, h   : bf16, or fp32 if residual_f32 = 1, [T][ldx], [T][ldh]
+ *   y      : bf16 [T][ldy] or NULL;  w_post : bf16 [N] or NULL (needs y);  w_pre : bf16 [N]
+ *   gate   : bf16 [N] with ld_gate = 0, or [T][ld_gate], or NULL (needs y)
+ *   z      : bf16 [T][ldz];  q : e4m3 [T][ldq], sf : uint32 [ceil(N/512)][ld_sf], quantized as
+ *            fp8_quant_group_pack quantizes the fp32 values (N % 128 == 0, ldq % 16 == 0)
+ *   N % 8 == 0, N <= 16384, leading dimensions >= N and % 8 == 0, ld_sf >= T.
+ * Backward: from d_z (bf16) and the gradient d_h of h that the residual stream brings (its
+ * type; NULL: none), with h as the forward wrote it, the gradients d_x (type of x), d_y (bf16),
+ * d_w_pre and d_w_post (fp32 [N]) and d_gate (fp32 [N] if ld_gate = 0, else bf16
+ * [T][ld_dgate]).  Those of parts that the forward has not are NULL.  The sums over the tokens
+ * are taken in a fixed order: equal calls give equal bits.  Their partial sums (at most
+ * 12 * 256 * N bytes) go to the library's per-(device, stream) workspace (FP8BS_ERR_ALLOC if
+ * it has to grow during HIP graph capture).  T == 0 sets the weights' gradients to zero.
+ */
+int residual_rms_norm(const void* x, int64_t ldx, int32_t residual_f32, const void* y, int64_t ldy, const void* w_post,
+                      const void* gate, int64_t ld_gate, const void* w_pre, float residual_scale, float eps,
+                      float weight_offset, int64_t T, int64_t N, void* h, int64_t ldh, void* z, int64_t ldz, void* q,
+                      int64_t ldq, uint32_t* sf, int64_t ld_sf, void* stream);
+int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, int64_t ld_dh, const void* h,
+                               int64_t ldh, int32_t residual_f32, const void* y, int64_t ldy, const void* w_post,
+                               const void* gate, int64_t ld_gate, const void* w_pre, float residual_scale, float eps,
+                               float weight_offset, int64_t T, int64_t N, void* d_x, int64_t ld_dx, void* d_y,
+                               int64_t ld_dy, float* d_w_pre, float* d_w_post, void* d_gate, int64_t ld_dgate,
+                               void* stream);
+
+/*
+ * silu_mul_quant_group_pack that also keeps gate and up for the backward pass in 8 bits:
+ *   cq  : e4m3 [E][M_max][2H], gate then up, quantized as fp8_quant_group_pack does
+ *   csf : uint32 [E][2 * ceil(H/512)][M_max]: the words of gate, then the words of up
+ * x, masked_m, q and sf as there; q and sf are the same bits.  E <= 1024.
+ * Backward from the checkpoint: with s = sigmoid(gate) of the decoded values, for the valid rows
+ *   d_gate = d_y * up * s * (1 + gate * (1 - s)),   d_up = d_y * gate * s
+ *   d_y : bf16 [E][M_max][H];  d_x : bf16 [E][M_max][2H] out, or, with d_x = NULL, q e4m3
+ *   [E][M_max][2H] and sf uint32 [E][ceil(2H/512)][M_max] (the masked GEMM's layout for K = 2H).
+ */
+int silu_mul_quant_group_pack_checkpoint(const void* x, const int32_t* masked_m, int64_t E, int64_t M_max, int64_t H,
+                                         void* q, uint32_t* sf, void* cq, uint32_t* csf, void* stream);
+int silu_mul_backward_from_checkpoint(const void* d_y, const int32_t* masked_m, int64_t E, int64_t M_max, int64_t H,
+                                      const void* cq, const uint32_t* csf, void* d_x, void* q, uint32_t* sf,
+                                      void* stream);
+
 /* Status helpers. */
 const char* fp8bs_status_string(int status);
 int fp8bs_last_hip_error(void);
