@@ -54,23 +54,46 @@ def _rows(t, name, dtypes, rows, cols):
     return t.data_ptr(), ld
 
 
+def _out(t, name, dtypes, shape, like):
+    """An output the caller may have passed, or a new one of dtypes[0] beside `like`; its address."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtypes[0])
+        return t, t.data_ptr()
+    return t, _whole(t, name, dtypes, shape)
+
+
+def _out_rows(t, name, dtypes, rows, cols, like):
+    """The same of a 2-D output that may be strided; its address and row stride."""
+    if t is None:
+        t = like.new_empty((rows, cols), dtype=dtypes[0])
+        return t, t.data_ptr(), cols
+    return t, *_rows(t, name, dtypes, rows, cols)
+
+
 def _2d(t, name):
     if t.dim() != 2:
         raise ValueError("%s must have 2 dims, got %d" % (name, t.dim()))
     return t.shape
 
 
+# The raw handle of the current stream: a fifth of the cost of building a Stream object for
+# it (2.7 us on the measured host), which a single-token call would notice.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _launch(name, stream, tensors, *args):
-    """Calls the library on `stream` (None: the current one) once every tensor is known to
-    lie on the current device."""
+    """Calls the library on `stream` (None: the current one) once every tensor that the caller
+    passed is known to lie on the current device."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
-            raise ValueError("%s: every tensor must be a device tensor, all on one device" % name)
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError("%s: every tensor must be a device tensor, all on one device" % name)
     if dev != torch.cuda.current_device():
         raise ValueError("%s: the tensors are on cuda:%d, which is not the current device" % (name, dev))
     if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
+        stream = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     st = getattr(_lib, name)(*args, int(stream))
@@ -92,12 +115,8 @@ def moe_route_topk(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = 
     if scoring not in _SCORING:
         raise ValueError("scoring must be 'sigmoid' or 'softmax', got %r" % (scoring,))
     pb = None if bias is None else _whole(bias, "bias", _F32, (E,))
-    if topk_ids is None:
-        topk_ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-    pi = _whole(topk_ids, "topk_ids", _I32, (T, topk))
-    pw = _whole(weights, "weights", _F32, (T, topk))
+    topk_ids, pi = _out(topk_ids, "topk_ids", _I32, (T, topk), logits)
+    weights, pw = _out(weights, "weights", _F32, (T, topk), logits)
     _launch("moe_route_topk", stream, (logits, bias, topk_ids, weights), pl, logits.dtype == torch.float32, ld, T, E, pb,
             _SCORING[scoring], groups, topk_groups, group_top, topk, bool(renormalize), scale, pi, pw)
     return topk_ids, weights
@@ -115,9 +134,7 @@ def moe_route_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, d_weig
         raise ValueError("scoring must be 'sigmoid' or 'softmax', got %r" % (scoring,))
     pi = _whole(topk_ids, "topk_ids", _I32, (T, topk))
     pw = _whole(d_weights, "d_weights", _F32, (T, topk))
-    if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    pd, ld_d = _rows(d_logits, "d_logits", (logits.dtype,), T, E)
+    d_logits, pd, ld_d = _out_rows(d_logits, "d_logits", (logits.dtype,), T, E, logits)
     _launch("moe_route_topk_backward", stream, (logits, topk_ids, d_weights, d_logits), pl,
             logits.dtype == torch.float32, ld, T, E, pi, pw, _SCORING[scoring], topk, bool(renormalize), scale, pd, ld_d)
     return d_logits
@@ -137,9 +154,7 @@ def moe_combine(y: torch.Tensor, topk_ids: torch.Tensor, slot_of: torch.Tensor, 
     ps = _whole(slot_of, "slot_of", _I32, (T, topk))
     pw = None if weights is None else _whole(weights, "weights", _F32, (T, topk))
     pb, ld_b = (None, 0) if base is None else _rows(base, "base", _BF16, T, N)
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=y.device)
-    po, ld_o = _rows(out, "out", _BF16, T, N)
+    out, po, ld_o = _out_rows(out, "out", _BF16, T, N, y)
     _launch("moe_combine", stream, (y, topk_ids, slot_of, weights, base, out), py, pi, ps, pw, pb, ld_b, T, topk, E,
             M_max, N, po, ld_o)
     return out
@@ -163,27 +178,19 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, topk_ids: torch.T
     pw = pdw = None
     if weights is not None:
         pw = _whole(weights, "weights", _F32, (T, topk))
-        if d_weights is None:
-            d_weights = torch.empty((T, topk), dtype=torch.float32, device=y.device)
-        pdw = _whole(d_weights, "d_weights", _F32, (T, topk))
+        d_weights, pdw = _out(d_weights, "d_weights", _F32, (T, topk), y)
     elif d_weights is not None:
         raise ValueError("d_weights without weights")
     pdy = pq = psf = None
     if quantize:
         if d_y is not None:
             raise ValueError("d_y is not written with quantize")
-        if q is None:
-            q = torch.empty((E, M_max, N), dtype=torch.uint8, device=y.device)
-        if sf is None:
-            sf = torch.empty((E, _words(N), M_max), dtype=torch.int32, device=y.device)
-        pq = _whole(q, "q", _E4M3, (E, M_max, N))
-        psf = _whole(sf, "sf", _U32, (E, _words(N), M_max))
+        q, pq = _out(q, "q", _E4M3, (E, M_max, N), y)
+        sf, psf = _out(sf, "sf", _U32, (E, _words(N), M_max), y)
     else:
         if q is not None or sf is not None:
             raise ValueError("q and sf are written with quantize only")
-        if d_y is None:
-            d_y = torch.empty((E, M_max, N), dtype=torch.bfloat16, device=y.device)
-        pdy = _whole(d_y, "d_y", _BF16, (E, M_max, N))
+        d_y, pdy = _out(d_y, "d_y", _BF16, (E, M_max, N), y)
     _launch("moe_combine_backward", stream, (d_out, y, topk_ids, slot_of, weights, d_y, q, sf, d_weights), pd, ld_d, py,
             pi, ps, pw, T, topk, E, M_max, N, pdy, pq, psf, pdw)
     return (q, sf, d_weights) if quantize else (d_y, d_weights)
@@ -215,7 +222,6 @@ def residual_rms_norm(x: torch.Tensor, w_pre: torch.Tensor, y: torch.Tensor | No
     if out not in _OUT:
         raise ValueError("out must be 'bf16', 'fp8' or 'both', got %r" % (out,))
     want_z, want_q = _OUT[out]
-    dev = x.device
     if y is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate apply to y")
     py, ldy = (None, 0) if y is None else _rows(y, "y", _BF16, T, N)
@@ -223,23 +229,17 @@ def residual_rms_norm(x: torch.Tensor, w_pre: torch.Tensor, y: torch.Tensor | No
     pw = _whole(w_pre, "w_pre", _BF16, (N,))
     pg, ld_g = _gate(gate, T, N)
     ph, ldh, pz, ldz, pq, ldq, psf, ld_sf = None, 0, None, 0, None, 0, None, 0
-    if h is None and (y is not None or residual_scale != 1.0):
-        h = torch.empty((T, N), dtype=x.dtype, device=dev)
-    if h is not None:
-        ph, ldh = _rows(h, "h", (x.dtype,), T, N)
+    if h is not None or y is not None or residual_scale != 1.0:
+        h, ph, ldh = _out_rows(h, "h", (x.dtype,), T, N, x)
     if want_z:
-        if z is None:
-            z = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-        pz, ldz = _rows(z, "z", _BF16, T, N)
+        z, pz, ldz = _out_rows(z, "z", _BF16, T, N, x)
     elif z is not None:
         raise ValueError("z is not written with out=%r" % out)
     if want_q:
         W = _words(N)
-        if q is None:
-            q = torch.empty((T, N), dtype=torch.uint8, device=dev)
+        q, pq, ldq = _out_rows(q, "q", _E4M3, T, N, x)
         if sf is None:
-            sf = torch.empty((W, max(4, (T + 3) // 4 * 4)), dtype=torch.int32, device=dev)
-        pq, ldq = _rows(q, "q", _E4M3, T, N)
+            sf = x.new_empty((W, max(4, (T + 3) // 4 * 4)), dtype=torch.int32)
         _typed(sf, "sf", _U32)
         if sf.dim() != 2 or sf.shape[0] != W or sf.shape[1] < T or sf.stride(1) != 1 or sf.stride(0) < T:
             raise ValueError("sf must be [%d, >= %d] with unit column stride, got shape %s strides %s"
@@ -263,7 +263,6 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
     gradient d_h, of h's type) -> (d_x, d_y, d_w_pre, d_w_post, d_gate), None for parts that are not there.  d_x has h's
     type, d_y is bf16, the weights' gradients are fp32 [N]; d_gate is fp32 [N] for a gate [N] and bf16 [T, N] else."""
     T, N = _2d(h, "h")
-    dev = h.device
     pz, ld_z = _rows(d_z, "d_z", _BF16, T, N)
     ph, ldh = _rows(h, "h", _FLOAT, T, N)
     pdh, ld_dh = (None, 0) if d_h is None else _rows(d_h, "d_h", (h.dtype,), T, N)
@@ -275,30 +274,18 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
     pw = _whole(w_pre, "w_pre", _BF16, (N,))
     pwp = None if w_post is None else _whole(w_post, "w_post", _BF16, (N,))
     pg, ld_g = _gate(gate, T, N)
-    if d_x is None:
-        d_x = torch.empty((T, N), dtype=h.dtype, device=dev)
-    pdx, ld_dx = _rows(d_x, "d_x", (h.dtype,), T, N)
-    if d_w_pre is None:
-        d_w_pre = torch.empty((N,), dtype=torch.float32, device=dev)
-    pdw = _whole(d_w_pre, "d_w_pre", _F32, (N,))
+    d_x, pdx, ld_dx = _out_rows(d_x, "d_x", (h.dtype,), T, N, h)
+    d_w_pre, pdw = _out(d_w_pre, "d_w_pre", _F32, (N,), h)
     pdy, ld_dy, pdwp, pdg, ld_dg = None, 0, None, None, 0
     if y is not None:
-        if d_y is None:
-            d_y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-        pdy, ld_dy = _rows(d_y, "d_y", _BF16, T, N)
+        d_y, pdy, ld_dy = _out_rows(d_y, "d_y", _BF16, T, N, h)
     if w_post is not None:
-        if d_w_post is None:
-            d_w_post = torch.empty((N,), dtype=torch.float32, device=dev)
-        pdwp = _whole(d_w_post, "d_w_post", _F32, (N,))
+        d_w_post, pdwp = _out(d_w_post, "d_w_post", _F32, (N,), h)
     if gate is not None:
         if gate.dim() == 1:
-            if d_gate is None:
-                d_gate = torch.empty((N,), dtype=torch.float32, device=dev)
-            pdg = _whole(d_gate, "d_gate", _F32, (N,))
+            d_gate, pdg = _out(d_gate, "d_gate", _F32, (N,), h)
         else:
-            if d_gate is None:
-                d_gate = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-            pdg, ld_dg = _rows(d_gate, "d_gate", _BF16, T, N)
+            d_gate, pdg, ld_dg = _out_rows(d_gate, "d_gate", _BF16, T, N, h)
     _launch("residual_rms_norm_backward", stream,
             (d_z, d_h, h, y, w_post, gate, w_pre, d_x, d_y, d_w_pre, d_w_post, d_gate), pz, ld_z, pdh, ld_dh, ph, ldh,
             h.dtype == torch.float32, py, ldy, pwp, pg, ld_g, pw, residual_scale, eps, weight_offset, T, N, pdx, ld_dx,
@@ -318,18 +305,12 @@ def silu_mul_quant_group_pack_checkpoint(x: torch.Tensor, masked_m: torch.Tensor
     H, W = H2 // 2, _words(H2 // 2)
     px = _whole(x, "x", _BF16, x.shape)
     pm = _whole(masked_m, "masked_m", _I32, (E,))
-    dev = x.device
-    if q is None:
-        q = torch.empty((E, M_max, H), dtype=torch.uint8, device=dev)
-    if sf is None:
-        sf = torch.empty((E, W, M_max), dtype=torch.int32, device=dev)
-    if cq is None:
-        cq = torch.empty((E, M_max, H2), dtype=torch.uint8, device=dev)
-    if csf is None:
-        csf = torch.empty((E, 2 * W, M_max), dtype=torch.int32, device=dev)
-    _launch("silu_mul_quant_group_pack_checkpoint", stream, (x, masked_m, q, sf, cq, csf), px, pm, E, M_max, H,
-            _whole(q, "q", _E4M3, (E, M_max, H)), _whole(sf, "sf", _U32, (E, W, M_max)),
-            _whole(cq, "cq", _E4M3, (E, M_max, H2)), _whole(csf, "csf", _U32, (E, 2 * W, M_max)))
+    q, pq = _out(q, "q", _E4M3, (E, M_max, H), x)
+    sf, psf = _out(sf, "sf", _U32, (E, W, M_max), x)
+    cq, pc = _out(cq, "cq", _E4M3, (E, M_max, H2), x)
+    csf, pcs = _out(csf, "csf", _U32, (E, 2 * W, M_max), x)
+    _launch("silu_mul_quant_group_pack_checkpoint", stream, (x, masked_m, q, sf, cq, csf), px, pm, E, M_max, H, pq, psf,
+            pc, pcs)
     return q, sf, cq, csf
 
 
@@ -347,23 +328,16 @@ def silu_mul_backward_from_checkpoint(d_y: torch.Tensor, masked_m: torch.Tensor,
     pm = _whole(masked_m, "masked_m", _I32, (E,))
     pc = _whole(cq, "cq", _E4M3, (E, M_max, 2 * H))
     pcs = _whole(csf, "csf", _U32, (E, 2 * W, M_max))
-    dev = d_y.device
     px = pq = psf = None
     if quantize:
         if d_x is not None:
             raise ValueError("d_x is not written with quantize")
-        if q is None:
-            q = torch.empty((E, M_max, 2 * H), dtype=torch.uint8, device=dev)
-        if sf is None:
-            sf = torch.empty((E, _words(2 * H), M_max), dtype=torch.int32, device=dev)
-        pq = _whole(q, "q", _E4M3, (E, M_max, 2 * H))
-        psf = _whole(sf, "sf", _U32, (E, _words(2 * H), M_max))
+        q, pq = _out(q, "q", _E4M3, (E, M_max, 2 * H), d_y)
+        sf, psf = _out(sf, "sf", _U32, (E, _words(2 * H), M_max), d_y)
     else:
         if q is not None or sf is not None:
             raise ValueError("q and sf are written with quantize only")
-        if d_x is None:
-            d_x = torch.empty((E, M_max, 2 * H), dtype=torch.bfloat16, device=dev)
-        px = _whole(d_x, "d_x", _BF16, (E, M_max, 2 * H))
+        d_x, px = _out(d_x, "d_x", _BF16, (E, M_max, 2 * H), d_y)
     _launch("silu_mul_backward_from_checkpoint", stream, (d_y, masked_m, cq, csf, d_x, q, sf), pd, pm, E, M_max, H, pc,
             pcs, px, pq, psf)
     return (q, sf) if quantize else d_x

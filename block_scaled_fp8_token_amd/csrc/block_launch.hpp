@@ -70,7 +70,7 @@ struct NormGradients {
 };
 // partials: norm_backward_scratch_bytes() of device memory.
 hipError_t launch_norm_backward(const NormProblem& p, const NormGradients& g, float* partials, hipStream_t stream);
-size_t norm_backward_scratch_bytes(const NormProblem& p, const NormGradients& g);
+size_t norm_backward_scratch_bytes(const NormProblem& p);
 
 // 8-bit activation checkpoint of the gated activation, over a masked expert batch.
 constexpr int64_t kCheckpointMaxE = 1024;

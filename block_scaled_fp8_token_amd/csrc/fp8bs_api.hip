@@ -307,6 +307,7 @@ fp8bs::NormProblem norm_problem(int32_t residual_f32, const void* y, int64_t ldy
                                 int64_t ld_gate, const void* w_pre, float residual_scale, float eps, float offset,
                                 int64_t T, int64_t N) {
   fp8bs::NormProblem p;
+  if (gate == nullptr) ld_gate = 0;  // ld_gate != 0 means a gate row per token
   p.f32 = residual_f32 != 0;
   p.T = T;
   p.N = N;
@@ -790,7 +791,7 @@ int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, 
   // partial sums live in the stream's workspace past the split-K arrival counters
   const size_t off = fp8bs::gemm_workspace_zeroed_prefix();
   void* ws = nullptr;
-  st = get_workspace(off + fp8bs::norm_backward_scratch_bytes(p, g), static_cast<hipStream_t>(stream), &ws);
+  st = get_workspace(off + fp8bs::norm_backward_scratch_bytes(p), static_cast<hipStream_t>(stream), &ws);
   if (st != FP8BS_OK) return st;
   hipError_t e = fp8bs::launch_norm_backward(p, g, reinterpret_cast<float*>(static_cast<char*>(ws) + off),
                                              static_cast<hipStream_t>(stream));

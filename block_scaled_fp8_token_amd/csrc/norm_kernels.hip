@@ -9,6 +9,8 @@
 // A workgroup takes whole rows, its threads eight columns per chunk, and keeps a row in
 // registers from the first reduction to the last store, so each input is read once and
 // each output written once: bound by memory.
+#include <type_traits>
+
 #include "block_device.hpp"
 #include "block_launch.hpp"
 
@@ -16,104 +18,168 @@ namespace fp8bs {
 
 namespace {
 
-// Eight values of the residual stream (bf16 or fp32).
+// A row of the residual stream (bf16 or fp32).  Rows are addressed by a pointer that is
+// the same for the whole workgroup (scalar registers) and a 32-bit column per thread.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float* f) {
+using Stream = std::conditional_t<F32, float, uint16_t>;
+
+// Eight of its values, as loaded.
+template <bool F32>
+struct Raw {
+  u32x4 v[F32 ? 2 : 1];
+};
+__device__ __forceinline__ u32x4 load16(const void* row, uint32_t byte) {
+  return *reinterpret_cast<const u32x4*>(static_cast<const char*>(row) + byte);
+}
+__device__ __forceinline__ void store16(void* row, uint32_t byte, u32x4 v) {
+  *reinterpret_cast<u32x4*>(static_cast<char*>(row) + byte) = v;
+}
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_raw(const Stream<F32>* row, uint32_t col) {
+  Raw<F32> r;
   if constexpr (F32) {
-    const float* q = static_cast<const float*>(p) + i;
-    const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    r.v[0] = load16(row, col * 4);
+    r.v[1] = load16(row, col * 4 + 16);
   } else {
-    unpack_bf16x8(*reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i), f);
+    r.v[0] = load16(row, col * 2);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ Raw<F32> zero_raw() {
+  Raw<F32> r;
+#pragma unroll
+  for (u32x4& v : r.v) v = u32x4{0u, 0u, 0u, 0u};
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack_raw(const Raw<F32>& r, float* f) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.v[i / 4][i % 4]);
+  } else {
+    unpack_bf16x8(r.v[0], f);
   }
 }
 template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float* f) {
+__device__ __forceinline__ void store8(Stream<F32>* row, uint32_t col, const float* f) {
   if constexpr (F32) {
-    float* q = static_cast<float*>(p) + i;
-    *reinterpret_cast<float4*>(q) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(q + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    u32x4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = __float_as_uint(f[i]);
+      b[i] = __float_as_uint(f[4 + i]);
+    }
+    store16(row, col * 4, a);
+    store16(row, col * 4 + 16, b);
   } else {
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = pack_bf16x8(f);
+    store16(row, col * 2, pack_bf16x8(f));
   }
 }
-__device__ __forceinline__ void load_bf16x8(const uint16_t* p, float* f) {
-  unpack_bf16x8(*reinterpret_cast<const u32x4*>(p), f);
+__device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, uint32_t col) { return load16(row, col * 2); }
+
+// Keeps a register's contents from being known across loop trips, so that weights stay
+// packed in registers instead of being unpacked to twice as many outside the loop.
+__device__ __forceinline__ void keep_packed(u32x4& v) { asm volatile("" : "+v"(v)); }
+
+// One row as loaded, the chunks of one thread.  FULL: a gate of its own for every token.
+template <bool F32, bool FULL, int CH>
+struct NormRow {
+  Raw<F32> x[CH];
+  u32x4 y[CH], gate[FULL ? CH : 1];
+};
+template <bool F32, bool FULL, int CH>
+__device__ __forceinline__ void load_row(const NormProblem& p, const Stream<F32>* x, int64_t ldx, int64_t r,
+                                         NormRow<F32, FULL, CH>& row) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+    if (col < p.N) {
+      if (p.y != nullptr) row.y[c] = load_bf16x8(p.y + r * p.ldy, col);
+      row.x[c] = load_raw<F32>(x + r * ldx, col);
+      if constexpr (FULL) row.gate[c] = load_bf16x8(p.gate + r * p.ld_gate, col);
+    }
+  }
 }
 
-template <bool F32, int CH>
-__global__ __launch_bounds__(1024) void norm_kernel(NormProblem p, const void* __restrict__ x, int64_t ldx,
-                                                    void* __restrict__ h, int64_t ldh, uint16_t* __restrict__ z,
-                                                    int64_t ldz, uint8_t* __restrict__ q, int64_t ldq,
-                                                    uint32_t* __restrict__ sf, int64_t ld_sf) {
+template <bool F32, bool FULL, int CH>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(CH == 1 ? 7 : 4))) void norm_kernel(
+    NormProblem p, const Stream<F32>* __restrict__ x, int64_t ldx, Stream<F32>* __restrict__ h, int64_t ldh,
+    uint16_t* __restrict__ z, int64_t ldz, uint8_t* __restrict__ q, int64_t ldq, uint32_t* __restrict__ sf,
+    int64_t ld_sf) {
   __shared__ float part[2][16];
   const int waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63;
   const float inv_n = 1.0f / (float)p.N;
+  const u32x4 none = {0u, 0u, 0u, 0u};
   int turn = 0;  // of the halves of `part`: consecutive sums use different ones
+  NormRow<F32, FULL, CH> next;
+  u32x4 w_post[CH], w_pre[CH], gate[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+    next.x[c] = zero_raw<F32>();
+    next.y[c] = w_post[c] = w_pre[c] = gate[c] = none;
+    if constexpr (FULL) next.gate[c] = none;
+    if (col < p.N) {
+      w_pre[c] = load_bf16x8(p.w_pre, col);
+      if (p.w_post != nullptr) w_post[c] = load_bf16x8(p.w_post, col);
+      if (!FULL && p.gate != nullptr) gate[c] = load_bf16x8(p.gate, col);
+    }
+  }
+  load_row(p, x, ldx, blockIdx.x, next);
   for (int64_t r = blockIdx.x; r < p.T; r += gridDim.x) {
     float v[CH][8];
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
-    if (p.y != nullptr) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
-        if (col < p.N) load_bf16x8(p.y + r * p.ldy + col, v[c]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[c][i], v[c][i], ss);
-      }
-      float inv = 1.0f;
-      if (p.w_post != nullptr) inv = rsqrtf(block_sum(ss, part[turn ^= 1], waves) * inv_n + p.eps);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
-        if (col < p.N) {
-          float w[8];
-          if (p.w_post != nullptr) {
-            load_bf16x8(p.w_post + col, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] *= inv * (w[i] + p.offset);
-          }
-          if (p.gate != nullptr) {
-            load_bf16x8(p.gate + r * p.ld_gate + col, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
-          }
-        }
-      }
-    }
+    Raw<F32> xr[CH];
     float ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
-      if (col < p.N) {
-        float a[8];
-        load8<F32>(x, r * ldx + col, a);
+      keep_packed(w_post[c]);
+      keep_packed(w_pre[c]);
+      keep_packed(gate[c]);
+      unpack_bf16x8(next.y[c], v[c]);
+      xr[c] = next.x[c];
+      if constexpr (FULL) gate[c] = next.gate[c];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[c][i] = __builtin_fmaf(p.residual_scale, a[i], v[c][i]);
-          ss = __builtin_fmaf(v[c][i], v[c][i], ss);
-        }
-        if (h != nullptr) store8<F32>(h, r * ldh + col, v[c]);
-      }
+      for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[c][i], v[c][i], ss);
     }
-    const float inv = rsqrtf(block_sum(ss, part[turn ^= 1], waves) * inv_n + p.eps);
+    if (r + gridDim.x < p.T) load_row(p, x, ldx, r + gridDim.x, next);
+    __builtin_amdgcn_sched_barrier(0);  // the next row's loads go out before this row's reductions
+    float inv = 1.0f;
+    if (p.w_post != nullptr) inv = rsqrtf(block_sum(ss, part[turn ^= 1], waves) * inv_n + p.eps);
+    ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
-      const bool valid = col < p.N;
-      if (valid) {
-        float w[8];
-        load_bf16x8(p.w_pre + col, w);
+      const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+      float w[8];
+      if (p.w_post != nullptr) {
+        unpack_bf16x8(w_post[c], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[c][i] *= inv * (w[i] + p.offset);
-        if (z != nullptr) *reinterpret_cast<u32x4*>(z + r * ldz + col) = pack_bf16x8(v[c]);
       }
+      if (p.gate != nullptr) {
+        unpack_bf16x8(gate[c], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+      }
+      unpack_raw<F32>(xr[c], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] = __builtin_fmaf(p.residual_scale, w[i], v[c][i]);
+        ss = __builtin_fmaf(v[c][i], v[c][i], ss);
+      }
+      if (h != nullptr && col < p.N) store8<F32>(h + r * ldh, col, v[c]);
+    }
+    inv = rsqrtf(block_sum(ss, part[turn ^= 1], waves) * inv_n + p.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+      const bool valid = col < p.N;
+      float w[8];
+      unpack_bf16x8(w_pre[c], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= inv * (w[i] + p.offset);
+      if (z != nullptr && valid) store8<false>(z + r * ldz, col, v[c]);
       if (q != nullptr) {
         const int e = group_exponent(v[c]);
         const uint32_t word = scale_word(valid ? (uint32_t)(e + 127) : 0u);
@@ -146,78 +212,156 @@ __device__ __forceinline__ void block_sum2(float& a, float& b, float2* part, int
 // rows of the gradients of the weights (and of a gate shared by all tokens) in
 // registers; they go to partials [sums][gridDim.x][N], which norm_sums_kernel adds up
 // in a fixed order.
-template <bool F32, int CH>
-__global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, NormGradients g,
-                                                             float* __restrict__ partials) {
+template <bool F32, bool FULL>
+struct GradRow {
+  Raw<F32> h, d_h;
+  u32x4 d_z, y, gate;
+};
+template <bool F32, bool FULL>
+__device__ __forceinline__ void load_row(const NormProblem& p, const NormGradients& g, int64_t r, uint32_t col,
+                                         GradRow<F32, FULL>& row) {
+  if (col < p.N) {
+    row.h = load_raw<F32>(static_cast<const Stream<F32>*>(g.h) + r * g.ldh, col);
+    row.d_z = load_bf16x8(g.d_z + r * g.ld_dz, col);
+    if (g.d_h != nullptr) row.d_h = load_raw<F32>(static_cast<const Stream<F32>*>(g.d_h) + r * g.ld_dh, col);
+    if (p.y != nullptr) row.y = load_bf16x8(p.y + r * p.ldy, col);
+    if constexpr (FULL) row.gate = load_bf16x8(p.gate + r * p.ld_gate, col);
+  }
+}
+
+// Where the sums over the tokens go: rows of N of each of the three, one per workgroup.
+struct NormSums {
+  float *pre, *post, *gate;
+};
+
+// Registers: with one chunk per thread (AHEAD) the row and the weights stay in registers
+// and the next row is loaded while this one is worked on.  With two there is no room: each
+// phase loads what it needs, which the phases after the first find in the L2 cache.
+template <bool F32, bool FULL, int CH>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, NormGradients g, NormSums sums) {
+  constexpr bool AHEAD = CH == 1;
   __shared__ float2 part[2][16];
   const int waves = blockDim.x >> 6;
   const float inv_n = 1.0f / (float)p.N;
-  const bool shared_gate = p.gate != nullptr && p.ld_gate == 0;
-  float s_pre[CH][8], s_post[CH][8], s_gate[CH][8];
+  const u32x4 none = {0u, 0u, 0u, 0u};
+  // sums of d_w_pre and d_w_post: four floats of a thread per entry, [2][CH][2][blockDim]
+  extern __shared__ u32x4 lds_sums[];
+  float s_gate[CH][8];
+  const GradRow<F32, FULL> zeros = {zero_raw<F32>(), zero_raw<F32>(), none, none, none};
+  GradRow<F32, FULL> cur = zeros, next = zeros;
+  u32x4 kept[3] = {none, none, none};  // AHEAD: w_pre, w_post, a gate shared by the tokens
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_post[c][i] = s_gate[c][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) s_gate[c][i] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4 * CH; ++k) lds_sums[k * blockDim.x + threadIdx.x] = none;
+  auto sum_at = [&](int which, int c, int half) -> u32x4& {
+    return lds_sums[((which * CH + c) * 2 + half) * blockDim.x + threadIdx.x];
+  };
+  // adds eight terms to a sum in LDS; a thread touches its own entries only
+  auto add_sum = [&](int which, int c, const float* t) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      u32x4 v = sum_at(which, c, half);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + t[4 * half + i]);
+      sum_at(which, c, half) = v;
+    }
+  };
+  if constexpr (AHEAD) {
+    const uint32_t col = threadIdx.x * 8;
+    if (col < p.N) {
+      kept[0] = load_bf16x8(p.w_pre, col);
+      if (p.w_post != nullptr) kept[1] = load_bf16x8(p.w_post, col);
+      if (!FULL && p.gate != nullptr) kept[2] = load_bf16x8(p.gate, col);
+    }
+    load_row(p, g, blockIdx.x, col, next);
+  }
+  // eight of w_pre (which = 0), w_post (1) or a shared gate (2)
+  auto weights = [&](int which, int c, float* w) {
+    if constexpr (AHEAD) {
+      unpack_bf16x8(kept[which], w);
+    } else {
+      const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+      const uint16_t* from = which == 0 ? p.w_pre : (which == 1 ? p.w_post : p.gate);
+      unpack_bf16x8(col < p.N ? load_bf16x8(from, col) : none, w);
+    }
+  };
+  // the row of chunk c, at the start of each phase
+  auto row_of = [&](int c, int64_t r) {
+    if constexpr (AHEAD) {  // packed again, not unpacked values of the phase before
+      for (u32x4& v : cur.h.v) keep_packed(v);
+      keep_packed(cur.d_z);
+      keep_packed(cur.y);
+      for (u32x4& k : kept) keep_packed(k);
+    } else {
+      cur = zeros;
+      load_row(p, g, r, (c * blockDim.x + threadIdx.x) * 8, cur);
+    }
+  };
+  auto gates = [&](int c, float* w) {
+    if constexpr (FULL) unpack_bf16x8(cur.gate, w);
+    else weights(2, c, w);
+  };
   int turn = 0;  // of the halves of `part`: consecutive sums use different ones
   for (int64_t r = blockIdx.x; r < p.T; r += gridDim.x) {
-    float h[CH][8], u[CH][8];
+    if constexpr (AHEAD) {
+      cur = next;
+      if (r + gridDim.x < p.T) load_row(p, g, r + gridDim.x, threadIdx.x * 8, next);
+      __builtin_amdgcn_sched_barrier(0);  // the next row's loads go out before this row is worked on
+    }
     float ss = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
+      row_of(c, r);
+      float h[8], u[8], w[8];
+      unpack_raw<F32>(cur.h, h);
+      unpack_bf16x8(cur.d_z, u);
+      weights(0, c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[c][i] = u[c][i] = 0.0f;
-      if (col < p.N) {
-        float w[8];
-        load8<F32>(g.h, r * g.ldh + col, h[c]);
-        load_bf16x8(g.d_z + r * g.ld_dz + col, u[c]);
-        load_bf16x8(p.w_pre + col, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = __builtin_fmaf(h[c][i], h[c][i], ss);
-          dot = __builtin_fmaf(u[c][i] * (w[i] + p.offset), h[c][i], dot);
-        }
+      for (int i = 0; i < 8; ++i) {
+        ss = __builtin_fmaf(h[i], h[i], ss);
+        dot = __builtin_fmaf(u[i] * (w[i] + p.offset), h[i], dot);
       }
     }
     block_sum2(ss, dot, part[turn ^= 1], waves);
     const float rh = rsqrtf(ss * inv_n + p.eps);
     const float mean = dot * rh * inv_n;  // of u hh
-    float y[CH][8];
+    float d[CH][8];                       // dh
     float ss_y = 0.0f, dot_y = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
+      const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+      row_of(c, r);
+      float h[8], u[8], w[8], dx[8], t[8];
+      unpack_raw<F32>(cur.h, h);
+      unpack_bf16x8(cur.d_z, u);
+      weights(0, c, w);
+      unpack_raw<F32>(cur.d_h, d[c]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[c][i] = 0.0f;
-      if (col < p.N) {
-        float w[8], dh[8];
-        load_bf16x8(p.w_pre + col, w);
+      for (int i = 0; i < 8; ++i) {
+        const float hh = h[i] * rh;
+        t[i] = u[i] * hh;
+        d[c][i] += rh * (u[i] * (w[i] + p.offset) - hh * mean);
+        dx[i] = p.residual_scale * d[c][i];
+      }
+      add_sum(0, c, t);
+      if (col < p.N) store8<F32>(static_cast<Stream<F32>*>(g.d_x) + r * g.ld_dx, col, dx);
+      if (p.w_post != nullptr) {
+        weights(1, c, w);
+        unpack_bf16x8(cur.y, h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dh[i] = 0.0f;
-        if (g.d_h != nullptr) load8<F32>(g.d_h, r * g.ld_dh + col, dh);
+        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (w[i] + p.offset);
+        if (p.gate != nullptr) {
+          gates(c, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] *= w[i];
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float hh = h[c][i] * rh;
-          s_pre[c][i] = __builtin_fmaf(u[c][i], hh, s_pre[c][i]);
-          u[c][i] = dh[i] + rh * (u[c][i] * (w[i] + p.offset) - hh * mean);  // dh
-          dh[i] = p.residual_scale * u[c][i];
-        }
-        store8<F32>(g.d_x, r * g.ld_dx + col, dh);
-        if (p.y != nullptr) {
-          load_bf16x8(p.y + r * p.ldy + col, y[c]);
-          float gt[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = gt[i] = 1.0f;
-          if (p.gate != nullptr) load_bf16x8(p.gate + r * p.ld_gate + col, gt);
-          if (p.w_post != nullptr) {
-            load_bf16x8(p.w_post + col, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float v = u[c][i] * gt[i] * (w[i] + p.offset);
-              ss_y = __builtin_fmaf(y[c][i], y[c][i], ss_y);
-              dot_y = __builtin_fmaf(v, y[c][i], dot_y);
-            }
-          }
+          ss_y = __builtin_fmaf(h[i], h[i], ss_y);
+          dot_y = __builtin_fmaf(u[i], h[i], dot_y);
         }
       }
     }
@@ -230,125 +374,157 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
-      if (col < p.N) {
-        float w[8], gt[8], dy[8], dg[8];
+      const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
+      row_of(c, r);
+      float y[8], w[8], gt[8], dy[8], dg[8], t[8];
+      unpack_bf16x8(cur.y, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = gt[i] = 1.0f;
-        if (p.gate != nullptr) load_bf16x8(p.gate + r * p.ld_gate + col, gt);
+      for (int i = 0; i < 8; ++i) w[i] = gt[i] = 1.0f;
+      if (p.gate != nullptr) gates(c, gt);
+      if (p.w_post != nullptr) {
+        weights(1, c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] += p.offset;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float yh = y[i] * ry, db = d[c][i] * gt[i];
+        dg[i] = d[c][i] * yh * w[i];
+        if constexpr (!FULL) s_gate[c][i] += dg[i];
         if (p.w_post != nullptr) {
-          load_bf16x8(p.w_post + col, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] += p.offset;
+          t[i] = db * yh;
+          dy[i] = ry * (db * w[i] - yh * mean_y);
+        } else {
+          dy[i] = db;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float yh = y[c][i] * ry, db = u[c][i] * gt[i];
-          dg[i] = u[c][i] * yh * w[i];
-          s_gate[c][i] += dg[i];
-          if (p.w_post != nullptr) {
-            s_post[c][i] = __builtin_fmaf(db, yh, s_post[c][i]);
-            dy[i] = ry * (db * w[i] - yh * mean_y);
-          } else {
-            dy[i] = db;
-          }
-        }
-        store8<false>(g.d_y, r * g.ld_dy + col, dy);
-        if (p.gate != nullptr && !shared_gate) store8<false>(g.d_gate, r * g.ld_dgate + col, dg);
+      }
+      if (p.w_post != nullptr) add_sum(1, c, t);
+      if (col < p.N) {
+        store8<false>(g.d_y + r * g.ld_dy, col, dy);
+        if constexpr (FULL) store8<false>(static_cast<uint16_t*>(g.d_gate) + r * g.ld_dgate, col, dg);
       }
     }
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int64_t col = (int64_t)(c * blockDim.x + threadIdx.x) * 8;
+    const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
     if (col < p.N) {
-      float* to = partials + (int64_t)blockIdx.x * p.N;
-      const int64_t next = (int64_t)gridDim.x * p.N;
-      store8<true>(to, col, s_pre[c]);
-      if (p.w_post != nullptr) {
-        to += next;
-        store8<true>(to, col, s_post[c]);
+      const int64_t row = (int64_t)blockIdx.x * p.N;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        store16(sums.pre + row, col * 4 + 16 * half, sum_at(0, c, half));
+        if (sums.post != nullptr) store16(sums.post + row, col * 4 + 16 * half, sum_at(1, c, half));
       }
-      if (shared_gate) store8<true>(to + next, col, s_gate[c]);
+      if (!FULL && sums.gate != nullptr) store8<true>(sums.gate + row, col, s_gate[c]);
     }
   }
 }
 
-// Sums of the partials: 64 columns per workgroup, its four wavefronts a quarter of the
-// rows each, joined in a fixed order.
-__global__ __launch_bounds__(256) void norm_sums_kernel(const float* __restrict__ partials, int rows, int64_t N,
-                                                        float* __restrict__ a, float* __restrict__ b,
-                                                        float* __restrict__ c) {
-  __shared__ float part[4][64];
+// Sums of the partials of every workgroup, in a fixed order: 64 columns per workgroup of
+// sixteen wavefronts, each of which adds every sixteenth row with eight loads in flight.
+__global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict__ partials, int rows, int64_t N,
+                                                         float* __restrict__ a, float* __restrict__ b,
+                                                         float* __restrict__ c) {
+  __shared__ float part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + lane;
-  const float* from = partials + (int64_t)blockIdx.y * rows * N;
+  const float* from = partials + (int64_t)blockIdx.y * rows * N + col;
   float s = 0.0f;
   if (col < N)
-    for (int r = wave; r < rows; r += 4) s += from[(int64_t)r * N + col];
+    for (int r0 = wave; r0 < rows; r0 += 128) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = r0 + 16 * k < rows ? from[(int64_t)(r0 + 16 * k) * N] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
   part[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && col < N) {
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += part[k][lane];
     float* to = blockIdx.y == 0 ? a : (blockIdx.y == 1 ? b : c);
-    to[col] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    to[col] = s;
   }
 }
 
-int backward_blocks(const NormProblem& p) { return (int)(p.T < 256 ? p.T : 256); }
-int sums_of(const NormProblem& p) {
-  return 1 + (p.w_post != nullptr ? 1 : 0) + (p.gate != nullptr && p.ld_gate == 0 ? 1 : 0);
-}
+constexpr int kCUs = 256;
 
 // Threads of a workgroup whose threads hold ch chunks each.
 unsigned threads_for(int64_t N, int ch) { return (unsigned)(64 * ((N / 8 + 64 * ch - 1) / (64 * ch))); }
 
-template <bool F32>
-hipError_t norm_as(const NormProblem& p, const void* x, int64_t ldx, void* h, int64_t ldh, uint16_t* z, int64_t ldz,
-                   uint8_t* q, int64_t ldq, uint32_t* sf, int64_t ld_sf, hipStream_t stream) {
-  const unsigned blocks = (unsigned)(p.T < 65536 ? p.T : 65536);
-  if (p.N <= 8192)
-    hipLaunchKernelGGL((norm_kernel<F32, 1>), dim3(blocks), dim3(threads_for(p.N, 1)), 0, stream, p, x, ldx, h, ldh, z,
-                       ldz, q, ldq, sf, ld_sf);
-  else
-    hipLaunchKernelGGL((norm_kernel<F32, 2>), dim3(blocks), dim3(threads_for(p.N, 2)), 0, stream, p, x, ldx, h, ldh, z,
-                       ldz, q, ldq, sf, ld_sf);
-  return hipGetLastError();
+// Chunks per thread: rows of up to 1024 threads' one chunk, else two.
+int chunks_for(int64_t N) { return N <= 8192 ? 1 : 2; }
+
+// Workgroups of the backward pass: as many as fit a compute unit's registers (16
+// wavefronts), four at the most, as each writes one row of partial sums.
+int backward_blocks(const NormProblem& p) {
+  const int per_cu = 1024 / (int)threads_for(p.N, chunks_for(p.N));
+  const int64_t fit = (int64_t)kCUs * (per_cu < 4 ? per_cu : 4);
+  return (int)(p.T < fit ? p.T : fit);
+}
+
+template <bool V>
+using Bool = std::integral_constant<bool, V>;
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// fn(Bool<F32>, Bool<FULL>, Int<CH>) for the types and the size of a problem.
+template <typename Fn>
+hipError_t by_shape(const NormProblem& p, Fn fn) {
+  auto chunks = [&](auto f32, auto full) {
+    return chunks_for(p.N) == 1 ? fn(f32, full, Int<1>{}) : fn(f32, full, Int<2>{});
+  };
+  if (p.f32) return p.ld_gate != 0 ? chunks(Bool<true>{}, Bool<true>{}) : chunks(Bool<true>{}, Bool<false>{});
+  return p.ld_gate != 0 ? chunks(Bool<false>{}, Bool<true>{}) : chunks(Bool<false>{}, Bool<false>{});
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormProblem& p, const void* x, int64_t ldx, void* h, int64_t ldh, uint16_t* z,
                        int64_t ldz, uint8_t* q, int64_t ldq, uint32_t* sf, int64_t ld_sf, hipStream_t stream) {
-  return p.f32 ? norm_as<true>(p, x, ldx, h, ldh, z, ldz, q, ldq, sf, ld_sf, stream)
-               : norm_as<false>(p, x, ldx, h, ldh, z, ldz, q, ldq, sf, ld_sf, stream);
+  return by_shape(p, [&](auto f32, auto full, auto ch) {
+    using S = Stream<f32.value>;
+    const unsigned threads = threads_for(p.N, ch.value);
+    // as many workgroups as fit on the chip at once
+    const int64_t fit = (int64_t)kCUs * ((ch.value == 1 ? 28 : 16) * 64 / threads);
+    hipLaunchKernelGGL((norm_kernel<f32.value, full.value, ch.value>), dim3((unsigned)(p.T < fit ? p.T : fit)),
+                       dim3(threads), 0, stream, p, static_cast<const S*>(x), ldx, static_cast<S*>(h), ldh, z, ldz, q,
+                       ldq, sf, ld_sf);
+    return hipGetLastError();
+  });
 }
 
-size_t norm_backward_scratch_bytes(const NormProblem& p, const NormGradients&) {
-  return (size_t)sums_of(p) * backward_blocks(p) * p.N * sizeof(float);
+size_t norm_backward_scratch_bytes(const NormProblem& p) {
+  const int blocks = backward_blocks(p);
+  return blocks > 1 ? 3 * (size_t)blocks * p.N * sizeof(float) : 0;
 }
 
 hipError_t launch_norm_backward(const NormProblem& p, const NormGradients& g, float* partials, hipStream_t stream) {
   const int blocks = backward_blocks(p);
-  const dim3 grid((unsigned)blocks);
-  if (p.N <= 8192) {
-    if (p.f32)
-      hipLaunchKernelGGL((norm_backward_kernel<true, 1>), grid, dim3(threads_for(p.N, 1)), 0, stream, p, g, partials);
-    else
-      hipLaunchKernelGGL((norm_backward_kernel<false, 1>), grid, dim3(threads_for(p.N, 1)), 0, stream, p, g, partials);
-  } else {
-    if (p.f32)
-      hipLaunchKernelGGL((norm_backward_kernel<true, 2>), grid, dim3(threads_for(p.N, 2)), 0, stream, p, g, partials);
-    else
-      hipLaunchKernelGGL((norm_backward_kernel<false, 2>), grid, dim3(threads_for(p.N, 2)), 0, stream, p, g, partials);
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  float* sums[3] = {g.d_w_pre, nullptr, nullptr};
+  float* const d_gate = p.gate != nullptr && p.ld_gate == 0 ? static_cast<float*>(g.d_gate) : nullptr;
+  // the sums that are wanted, in order; one workgroup has no partial sums to be joined
+  float* to[3] = {g.d_w_pre, nullptr, nullptr};
   int n = 1;
-  if (p.w_post != nullptr) sums[n++] = g.d_w_post;
-  if (p.gate != nullptr && p.ld_gate == 0) sums[n++] = static_cast<float*>(g.d_gate);
-  hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((p.N + 63) / 64), (unsigned)n), dim3(256), 0, stream, partials,
-                     blocks, p.N, sums[0], sums[1], sums[2]);
+  if (g.d_w_post != nullptr) to[n++] = g.d_w_post;
+  if (d_gate != nullptr) to[n++] = d_gate;
+  NormSums sums = {g.d_w_pre, g.d_w_post, d_gate};
+  if (blocks > 1) {
+    const int64_t one = (int64_t)blocks * p.N;
+    sums.pre = partials;
+    sums.post = g.d_w_post != nullptr ? partials + one : nullptr;
+    sums.gate = d_gate != nullptr ? partials + (n - 1) * one : nullptr;
+  }
+  hipError_t e = by_shape(p, [&](auto f32, auto full, auto ch) {
+    hipLaunchKernelGGL((norm_backward_kernel<f32.value, full.value, ch.value>), dim3((unsigned)blocks),
+                       dim3(threads_for(p.N, ch.value)), 4 * ch.value * 16 * threads_for(p.N, ch.value), stream, p, g,
+                       sums);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || blocks == 1) return e;
+  hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((p.N + 63) / 64), (unsigned)n), dim3(1024), 0, stream, partials,
+                     blocks, p.N, to[0], to[1], to[2]);
   return hipGetLastError();
 }
 
