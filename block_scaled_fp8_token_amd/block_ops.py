@@ -33,7 +33,8 @@ def _typed(t, name, dtypes):
 
 def _whole(t, name, dtypes, shape):
     """A contiguous tensor of that shape; its address."""
-    _typed(t, name, dtypes)
+    if t.dtype not in dtypes:
+        _typed(t, name, dtypes)
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s, got shape %s strides %s"
                          % (name, list(shape), list(t.shape), list(t.stride())))
@@ -42,7 +43,8 @@ def _whole(t, name, dtypes, shape):
 
 def _rows(t, name, dtypes, rows, cols):
     """A 2-D [rows, cols] tensor with unit column stride; its address and row stride."""
-    _typed(t, name, dtypes)
+    if t.dtype not in dtypes:
+        _typed(t, name, dtypes)
     if t.shape != (rows, cols):
         raise ValueError("%s must be %s, got %s" % (name, [rows, cols], list(t.shape)))
     ld, unit = t.stride()
@@ -54,11 +56,17 @@ def _rows(t, name, dtypes, rows, cols):
     return t.data_ptr(), ld
 
 
+def _beside(t, name, like):
+    if t.get_device() != like.get_device():
+        raise ValueError("%s: every tensor must be a device tensor, all on one device" % name)
+
+
 def _out(t, name, dtypes, shape, like):
     """An output the caller may have passed, or a new one of dtypes[0] beside `like`; its address."""
     if t is None:
         t = like.new_empty(shape, dtype=dtypes[0])
         return t, t.data_ptr()
+    _beside(t, name, like)
     return t, _whole(t, name, dtypes, shape)
 
 
@@ -67,6 +75,7 @@ def _out_rows(t, name, dtypes, rows, cols, like):
     if t is None:
         t = like.new_empty((rows, cols), dtype=dtypes[0])
         return t, t.data_ptr(), cols
+    _beside(t, name, like)
     return t, *_rows(t, name, dtypes, rows, cols)
 
 
@@ -76,27 +85,28 @@ def _2d(t, name):
     return t.shape
 
 
-# The raw handle of the current stream: a fifth of the cost of building a Stream object for
-# it (2.7 us on the measured host), which a single-token call would notice.
+# The raw handle of the current stream: building a Stream object for it costs 2.7 us on the
+# measured host, which a single-token call would notice.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _launch(name, stream, tensors, *args):
-    """Calls the library on `stream` (None: the current one) once every tensor that the caller
-    passed is known to lie on the current device."""
-    dev = tensors[0].get_device()
-    for t in tensors:
+def _launch(name, stream, inputs, *args):
+    """Calls the library on `stream` (None: the current one) once every input is known to lie on
+    the current device (the outputs lie beside an input, see _out)."""
+    dev = inputs[0].get_device()
+    for t in inputs:
         if t is not None and t.get_device() != dev:
             dev = -1
     if dev < 0:
         raise ValueError("%s: every tensor must be a device tensor, all on one device" % name)
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("%s: the tensors are on cuda:%d, which is not the current device" % (name, dev))
     if stream is None:
         stream = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    st = getattr(_lib, name)(*args, int(stream))
+    st = getattr(_lib, name)(*args, stream)
     if st:
         _check(name, st)
 
@@ -117,7 +127,7 @@ def moe_route_topk(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = 
     pb = None if bias is None else _whole(bias, "bias", _F32, (E,))
     topk_ids, pi = _out(topk_ids, "topk_ids", _I32, (T, topk), logits)
     weights, pw = _out(weights, "weights", _F32, (T, topk), logits)
-    _launch("moe_route_topk", stream, (logits, bias, topk_ids, weights), pl, logits.dtype == torch.float32, ld, T, E, pb,
+    _launch("moe_route_topk", stream, (logits, bias), pl, logits.dtype == torch.float32, ld, T, E, pb,
             _SCORING[scoring], groups, topk_groups, group_top, topk, bool(renormalize), scale, pi, pw)
     return topk_ids, weights
 
@@ -135,7 +145,7 @@ def moe_route_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, d_weig
     pi = _whole(topk_ids, "topk_ids", _I32, (T, topk))
     pw = _whole(d_weights, "d_weights", _F32, (T, topk))
     d_logits, pd, ld_d = _out_rows(d_logits, "d_logits", (logits.dtype,), T, E, logits)
-    _launch("moe_route_topk_backward", stream, (logits, topk_ids, d_weights, d_logits), pl,
+    _launch("moe_route_topk_backward", stream, (logits, topk_ids, d_weights), pl,
             logits.dtype == torch.float32, ld, T, E, pi, pw, _SCORING[scoring], topk, bool(renormalize), scale, pd, ld_d)
     return d_logits
 
@@ -155,7 +165,7 @@ def moe_combine(y: torch.Tensor, topk_ids: torch.Tensor, slot_of: torch.Tensor, 
     pw = None if weights is None else _whole(weights, "weights", _F32, (T, topk))
     pb, ld_b = (None, 0) if base is None else _rows(base, "base", _BF16, T, N)
     out, po, ld_o = _out_rows(out, "out", _BF16, T, N, y)
-    _launch("moe_combine", stream, (y, topk_ids, slot_of, weights, base, out), py, pi, ps, pw, pb, ld_b, T, topk, E,
+    _launch("moe_combine", stream, (y, topk_ids, slot_of, weights, base), py, pi, ps, pw, pb, ld_b, T, topk, E,
             M_max, N, po, ld_o)
     return out
 
@@ -191,7 +201,7 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, topk_ids: torch.T
         if q is not None or sf is not None:
             raise ValueError("q and sf are written with quantize only")
         d_y, pdy = _out(d_y, "d_y", _BF16, (E, M_max, N), y)
-    _launch("moe_combine_backward", stream, (d_out, y, topk_ids, slot_of, weights, d_y, q, sf, d_weights), pd, ld_d, py,
+    _launch("moe_combine_backward", stream, (d_out, y, topk_ids, slot_of, weights), pd, ld_d, py,
             pi, ps, pw, T, topk, E, M_max, N, pdy, pq, psf, pdw)
     return (q, sf, d_weights) if quantize else (d_y, d_weights)
 
@@ -240,14 +250,16 @@ def residual_rms_norm(x: torch.Tensor, w_pre: torch.Tensor, y: torch.Tensor | No
         q, pq, ldq = _out_rows(q, "q", _E4M3, T, N, x)
         if sf is None:
             sf = x.new_empty((W, max(4, (T + 3) // 4 * 4)), dtype=torch.int32)
-        _typed(sf, "sf", _U32)
+        else:
+            _beside(sf, "sf", x)
+            _typed(sf, "sf", _U32)
         if sf.dim() != 2 or sf.shape[0] != W or sf.shape[1] < T or sf.stride(1) != 1 or sf.stride(0) < T:
             raise ValueError("sf must be [%d, >= %d] with unit column stride, got shape %s strides %s"
                              % (W, T, list(sf.shape), list(sf.stride())))
         psf, ld_sf = sf.data_ptr(), sf.stride(0)
     elif q is not None or sf is not None:
         raise ValueError("q and sf are not written with out=%r" % out)
-    _launch("residual_rms_norm", stream, (x, y, w_post, gate, w_pre, h, z, q, sf), px, ldx, x.dtype == torch.float32, py,
+    _launch("residual_rms_norm", stream, (x, y, w_post, gate, w_pre), px, ldx, x.dtype == torch.float32, py,
             ldy, pwp, pg, ld_g, pw, residual_scale, eps, weight_offset, T, N, ph, ldh, pz, ldz, pq, ldq, psf, ld_sf)
     return x if h is None else h, z, q, sf
 
@@ -287,7 +299,7 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
         else:
             d_gate, pdg, ld_dg = _out_rows(d_gate, "d_gate", _BF16, T, N, h)
     _launch("residual_rms_norm_backward", stream,
-            (d_z, d_h, h, y, w_post, gate, w_pre, d_x, d_y, d_w_pre, d_w_post, d_gate), pz, ld_z, pdh, ld_dh, ph, ldh,
+            (d_z, d_h, h, y, w_post, gate, w_pre), pz, ld_z, pdh, ld_dh, ph, ldh,
             h.dtype == torch.float32, py, ldy, pwp, pg, ld_g, pw, residual_scale, eps, weight_offset, T, N, pdx, ld_dx,
             pdy, ld_dy, pdw, pdwp, pdg, ld_dg)
     return d_x, d_y, d_w_pre, d_w_post, d_gate
@@ -309,7 +321,7 @@ def silu_mul_quant_group_pack_checkpoint(x: torch.Tensor, masked_m: torch.Tensor
     sf, psf = _out(sf, "sf", _U32, (E, W, M_max), x)
     cq, pc = _out(cq, "cq", _E4M3, (E, M_max, H2), x)
     csf, pcs = _out(csf, "csf", _U32, (E, 2 * W, M_max), x)
-    _launch("silu_mul_quant_group_pack_checkpoint", stream, (x, masked_m, q, sf, cq, csf), px, pm, E, M_max, H, pq, psf,
+    _launch("silu_mul_quant_group_pack_checkpoint", stream, (x, masked_m), px, pm, E, M_max, H, pq, psf,
             pc, pcs)
     return q, sf, cq, csf
 
@@ -338,6 +350,6 @@ def silu_mul_backward_from_checkpoint(d_y: torch.Tensor, masked_m: torch.Tensor,
         if q is not None or sf is not None:
             raise ValueError("q and sf are written with quantize only")
         d_x, px = _out(d_x, "d_x", _BF16, (E, M_max, 2 * H), d_y)
-    _launch("silu_mul_backward_from_checkpoint", stream, (d_y, masked_m, cq, csf, d_x, q, sf), pd, pm, E, M_max, H, pc,
+    _launch("silu_mul_backward_from_checkpoint", stream, (d_y, masked_m, cq, csf), pd, pm, E, M_max, H, pc,
             pcs, px, pq, psf)
     return (q, sf) if quantize else d_x

@@ -285,7 +285,7 @@ fp8bs::RouteProblem route_problem(const void* logits, int32_t logits_f32, int64_
 // Sizes of the combine and its backward pass; 1: nothing to do.
 int check_combine(int64_t T, int32_t topk, int64_t E, int64_t M_max, int64_t N) {
   if (T < 0 || E < 0 || M_max < 0 || N < 0 || N % 8 != 0 || topk < 1 || topk > 64) return FP8BS_ERR_SHAPE;
-  if (T > INT32_MAX || E > INT32_MAX || M_max > INT32_MAX || T * ((N + 2047) / 2048) > INT32_MAX)
+  if (T > INT32_MAX || E > INT32_MAX || M_max > INT32_MAX || N > (1 << 30) || T * ((N + 2047) / 2048) > INT32_MAX)
     return FP8BS_ERR_SHAPE;
   return T == 0 || N == 0 ? 1 : FP8BS_OK;
 }
@@ -325,7 +325,7 @@ fp8bs::NormProblem norm_problem(int32_t residual_f32, const void* y, int64_t ldy
 
 int check_checkpoint(int64_t E, int64_t M_max, int64_t H) {
   if (E < 0 || E > fp8bs::kCheckpointMaxE || M_max < 0 || H < 0 || H % 128 != 0) return FP8BS_ERR_SHAPE;
-  if (E * M_max > INT32_MAX || M_max > INT32_MAX || H > INT32_MAX) return FP8BS_ERR_SHAPE;
+  if (M_max > INT32_MAX || E * M_max > INT32_MAX || H > (1 << 28)) return FP8BS_ERR_SHAPE;
   return E == 0 || M_max == 0 || H == 0 ? 1 : FP8BS_OK;
 }
 

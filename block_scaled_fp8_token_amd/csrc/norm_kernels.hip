@@ -28,21 +28,20 @@ template <bool F32>
 struct Raw {
   u32x4 v[F32 ? 2 : 1];
 };
+template <bool STREAM>
 __device__ __forceinline__ u32x4 load16(const void* row, uint32_t byte) {
-  return *reinterpret_cast<const u32x4*>(static_cast<const char*>(row) + byte);
+  const char* from = static_cast<const char*>(row) + byte;
+  if constexpr (STREAM) return load_stream(from);
+  return *reinterpret_cast<const u32x4*>(from);
 }
 __device__ __forceinline__ void store16(void* row, uint32_t byte, u32x4 v) {
-  *reinterpret_cast<u32x4*>(static_cast<char*>(row) + byte) = v;
+  store_stream(static_cast<char*>(row) + byte, v);
 }
-template <bool F32>
+template <bool F32, bool STREAM>
 __device__ __forceinline__ Raw<F32> load_raw(const Stream<F32>* row, uint32_t col) {
   Raw<F32> r;
-  if constexpr (F32) {
-    r.v[0] = load16(row, col * 4);
-    r.v[1] = load16(row, col * 4 + 16);
-  } else {
-    r.v[0] = load16(row, col * 2);
-  }
+#pragma unroll
+  for (int k = 0; k < (F32 ? 2 : 1); ++k) r.v[k] = load16<STREAM>(row, col * (F32 ? 4 : 2) + 16 * k);
   return r;
 }
 template <bool F32>
@@ -76,7 +75,14 @@ __device__ __forceinline__ void store8(Stream<F32>* row, uint32_t col, const flo
     store16(row, col * 2, pack_bf16x8(f));
   }
 }
-__device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, uint32_t col) { return load16(row, col * 2); }
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, uint32_t col) {
+  return load16<STREAM>(row, col * 2);
+}
+// Eight of a vector that every row uses.
+__device__ __forceinline__ u32x4 load_weights(const uint16_t* w, uint32_t col) {
+  return *reinterpret_cast<const u32x4*>(w + col);
+}
 
 // Keeps a register's contents from being known across loop trips, so that weights stay
 // packed in registers instead of being unpacked to twice as many outside the loop.
@@ -95,9 +101,9 @@ __device__ __forceinline__ void load_row(const NormProblem& p, const Stream<F32>
   for (int c = 0; c < CH; ++c) {
     const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
     if (col < p.N) {
-      if (p.y != nullptr) row.y[c] = load_bf16x8(p.y + r * p.ldy, col);
-      row.x[c] = load_raw<F32>(x + r * ldx, col);
-      if constexpr (FULL) row.gate[c] = load_bf16x8(p.gate + r * p.ld_gate, col);
+      if (p.y != nullptr) row.y[c] = load_bf16x8<true>(p.y + r * p.ldy, col);
+      row.x[c] = load_raw<F32, true>(x + r * ldx, col);
+      if constexpr (FULL) row.gate[c] = load_bf16x8<true>(p.gate + r * p.ld_gate, col);
     }
   }
 }
@@ -122,9 +128,9 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(CH == 1 ? 
     next.y[c] = w_post[c] = w_pre[c] = gate[c] = none;
     if constexpr (FULL) next.gate[c] = none;
     if (col < p.N) {
-      w_pre[c] = load_bf16x8(p.w_pre, col);
-      if (p.w_post != nullptr) w_post[c] = load_bf16x8(p.w_post, col);
-      if (!FULL && p.gate != nullptr) gate[c] = load_bf16x8(p.gate, col);
+      w_pre[c] = load_weights(p.w_pre, col);
+      if (p.w_post != nullptr) w_post[c] = load_weights(p.w_post, col);
+      if (!FULL && p.gate != nullptr) gate[c] = load_weights(p.gate, col);
     }
   }
   load_row(p, x, ldx, blockIdx.x, next);
@@ -181,9 +187,9 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(CH == 1 ? 
       for (int i = 0; i < 8; ++i) v[c][i] *= inv * (w[i] + p.offset);
       if (z != nullptr && valid) store8<false>(z + r * ldz, col, v[c]);
       if (q != nullptr) {
-        const int e = group_exponent(v[c]);
-        const uint32_t word = scale_word(valid ? (uint32_t)(e + 127) : 0u);
-        if (valid) *reinterpret_cast<uint64_t*>(q + r * ldq + col) = codes_at(v[c], e);
+        const uint32_t byte = group_byte(v[c]);
+        const uint32_t word = scale_word(valid ? byte : 0u);
+        if (valid) store_stream(q + r * ldq + col, codes_at(v[c], byte));
         if (lane == 0 && valid) sf[(col / 512) * ld_sf + r] = word;
       }
     }
@@ -221,11 +227,11 @@ template <bool F32, bool FULL>
 __device__ __forceinline__ void load_row(const NormProblem& p, const NormGradients& g, int64_t r, uint32_t col,
                                          GradRow<F32, FULL>& row) {
   if (col < p.N) {
-    row.h = load_raw<F32>(static_cast<const Stream<F32>*>(g.h) + r * g.ldh, col);
-    row.d_z = load_bf16x8(g.d_z + r * g.ld_dz, col);
-    if (g.d_h != nullptr) row.d_h = load_raw<F32>(static_cast<const Stream<F32>*>(g.d_h) + r * g.ld_dh, col);
-    if (p.y != nullptr) row.y = load_bf16x8(p.y + r * p.ldy, col);
-    if constexpr (FULL) row.gate = load_bf16x8(p.gate + r * p.ld_gate, col);
+    row.h = load_raw<F32, false>(static_cast<const Stream<F32>*>(g.h) + r * g.ldh, col);
+    row.d_z = load_bf16x8<false>(g.d_z + r * g.ld_dz, col);
+    if (g.d_h != nullptr) row.d_h = load_raw<F32, false>(static_cast<const Stream<F32>*>(g.d_h) + r * g.ld_dh, col);
+    if (p.y != nullptr) row.y = load_bf16x8<false>(p.y + r * p.ldy, col);
+    if constexpr (FULL) row.gate = load_bf16x8<false>(p.gate + r * p.ld_gate, col);
   }
 }
 
@@ -272,9 +278,9 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
   if constexpr (AHEAD) {
     const uint32_t col = threadIdx.x * 8;
     if (col < p.N) {
-      kept[0] = load_bf16x8(p.w_pre, col);
-      if (p.w_post != nullptr) kept[1] = load_bf16x8(p.w_post, col);
-      if (!FULL && p.gate != nullptr) kept[2] = load_bf16x8(p.gate, col);
+      kept[0] = load_weights(p.w_pre, col);
+      if (p.w_post != nullptr) kept[1] = load_weights(p.w_post, col);
+      if (!FULL && p.gate != nullptr) kept[2] = load_weights(p.gate, col);
     }
     load_row(p, g, blockIdx.x, col, next);
   }
@@ -285,7 +291,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
     } else {
       const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
       const uint16_t* from = which == 0 ? p.w_pre : (which == 1 ? p.w_post : p.gate);
-      unpack_bf16x8(col < p.N ? load_bf16x8(from, col) : none, w);
+      unpack_bf16x8(col < p.N ? load_weights(from, col) : none, w);
     }
   };
   // the row of chunk c, at the start of each phase
@@ -412,10 +418,12 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
       const int64_t row = (int64_t)blockIdx.x * p.N;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        store16(sums.pre + row, col * 4 + 16 * half, sum_at(0, c, half));
-        if (sums.post != nullptr) store16(sums.post + row, col * 4 + 16 * half, sum_at(1, c, half));
+        *reinterpret_cast<u32x4*>(sums.pre + row + col + 4 * half) = sum_at(0, c, half);
+        if (sums.post != nullptr) *reinterpret_cast<u32x4*>(sums.post + row + col + 4 * half) = sum_at(1, c, half);
+        if (!FULL && sums.gate != nullptr)
+          *reinterpret_cast<float4*>(sums.gate + row + col + 4 * half) =
+              make_float4(s_gate[c][4 * half], s_gate[c][4 * half + 1], s_gate[c][4 * half + 2], s_gate[c][4 * half + 3]);
       }
-      if (!FULL && sums.gate != nullptr) store8<true>(sums.gate + row, col, s_gate[c]);
     }
   }
 }

@@ -7,8 +7,10 @@
 // highest ranks are chosen, ties to the lowest index, and weighted by
 // scale * s, or scale * s / (sum of the chosen s).
 //
-// One wavefront routes one token: expert i * 64 + lane sits in register i of its lane,
-// so the loads are coalesced at any row stride and the selection needs no LDS.
+// Two kernels.  route_row_kernel, for up to eight of up to 256 experts: sixteen lanes route
+// one token, each lane sorts the ranks it holds, and four merges leave the token's eight
+// best in every lane.  route_kernel, for everything else: one wavefront routes one token
+// and takes one maximum per choice.
 #include <type_traits>
 
 #include "block_device.hpp"
@@ -51,6 +53,216 @@ __device__ __forceinline__ float group_score(float a, float b, int group_top) {
   return group_top == 2 && b > kNone ? a + b : a;
 }
 
+// ---- sixteen lanes per token ----
+//
+// A rank and its expert are one fp64 number: the fp32 rank is exact in its upper bits and
+// the low ten bits of its mantissa hold the expert so that of equal ranks the lower expert
+// is the larger number.  All numbers differ, a comparison of two is one instruction each for
+// the larger and the smaller, and ties need no case of their own.
+constexpr int kList = 8;             // ranks a lane keeps, sorted
+constexpr int kNoneHi = 0xC8078000;  // upper half of about -1e39: below every fp32
+
+// Experts of a token over the sixteen lanes of a row: a group (all experts where there are
+// no groups) has `lanes` of them, each takes `per_lane` consecutive experts of its group.
+struct RowLayout {
+  int lanes, per_lane;
+  int groups, size;
+  bool wide;  // a lane's logits are whole aligned 16-byte words
+};
+
+__device__ __forceinline__ double rank_of(float rank, int expert) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, (double)(rank + 0.0f));  // + 0: -0 ranks as 0
+  const int hi = (int)(u >> 32);
+  const uint32_t code = (uint32_t)((expert ^ 1023) ^ ((hi >> 31) & 1023));
+  const uint32_t top = (uint32_t)(rank > kNone ? hi : kNoneHi);
+  return __builtin_bit_cast(double, ((uint64_t)top << 32) | (uint32_t)u | code);
+}
+__device__ __forceinline__ double without_rank(double r) {
+  return __builtin_bit_cast(double, ((uint64_t)(uint32_t)kNoneHi << 32) | (uint32_t)__builtin_bit_cast(uint64_t, r));
+}
+// The expert of a rank, or -1.
+__device__ __forceinline__ int expert_of(double r) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, r);
+  const int hi = (int)(u >> 32);
+  return hi == kNoneHi ? -1 : (int)(((uint32_t)u & 1023) ^ 1023 ^ ((hi >> 31) & 1023));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ void order(double& a, double& b) {  // a >= b
+  const double lo = __builtin_fmin(a, b);
+  a = __builtin_fmax(a, b);
+  b = lo;
+}
+// Descending order of eight: Batcher's odd-even merge sort, 19 comparators.
+__device__ __forceinline__ void sort8(double* v) {
+  order(v[0], v[1]); order(v[2], v[3]); order(v[4], v[5]); order(v[6], v[7]);
+  order(v[0], v[2]); order(v[1], v[3]); order(v[4], v[6]); order(v[5], v[7]);
+  order(v[1], v[2]); order(v[5], v[6]);
+  order(v[0], v[4]); order(v[1], v[5]); order(v[2], v[6]); order(v[3], v[7]);
+  order(v[2], v[4]); order(v[3], v[5]);
+  order(v[1], v[2]); order(v[3], v[4]); order(v[5], v[6]);
+}
+// The eight largest of two descending lists, descending: the larger of opposite ends are
+// they, first falling, then rising, which three rounds of comparators straighten.
+__device__ __forceinline__ void merge8(double* v, const double* w) {
+#pragma unroll
+  for (int i = 0; i < kList; ++i) v[i] = __builtin_fmax(v[i], w[kList - 1 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < kList; ++i)
+      if (!(i & d)) order(v[i], v[i + d]);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_lanes(double* v) {
+  double w[kList];
+#pragma unroll
+  for (int i = 0; i < kList; ++i) w[i] = dpp_d<CTRL>(v[i]);
+  merge8(v, w);
+}
+// Groups (one number per lane, the same in all lanes of a group) ahead of the lane's own.
+template <int R>
+__device__ __forceinline__ int groups_ahead(double mine, int lanes) {
+  constexpr int kRowRor = 0x120;
+  int n = 0;
+  if (R % lanes == 0) n = dpp_d<kRowRor + R>(mine) > mine ? 1 : 0;  // uniform condition
+  if constexpr (R < 15) n += groups_ahead<R + 1>(mine, lanes);
+  return n;
+}
+
+// V logits of a lane from expert `first` on, `n` of them there.
+template <int V, bool F32>
+__device__ __forceinline__ void load_lane(const void* logits, int64_t row, int first, int n, bool wide, float* l) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = kNone;
+  if (wide) {  // uniform
+    constexpr int M = F32 ? 4 : 8;
+#pragma unroll
+    for (int i = 0; i < V; i += M)
+      if (i < n) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(logits) +
+                                                        (row + first + i) * (F32 ? 4 : 2));
+        if constexpr (F32) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l[i + k] = clean_logit(__uint_as_float(v[k]));
+        } else {
+          unpack_bf16x8(v, l + i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) l[i + k] = clean_logit(l[i + k]);
+        }
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) l[i] = clean_logit(load_logit<F32>(logits, row + first + i));
+  }
+}
+
+template <int V, bool F32, bool SOFTMAX>
+__global__ __launch_bounds__(64) void route_row_kernel(const void* __restrict__ logits, int64_t ld, int64_t T,
+                                                       RowLayout at, const float* __restrict__ bias, int topk_groups,
+                                                       int group_top, int topk, int renormalize, float scale,
+                                                       int32_t* __restrict__ ids, float* __restrict__ weights) {
+  const int sub = threadIdx.x & 15;
+  const int64_t token = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 4);
+  const int64_t t = token < T ? token : T - 1;  // rows past the end work on the last one and store nothing
+  const int group = sub / at.lanes, part = sub - group * at.lanes;
+  const int first = group * at.size + part * at.per_lane;
+  int n = at.size - part * at.per_lane;  // experts of this lane
+  n = group < at.groups ? (n < at.per_lane ? n : at.per_lane) : 0;
+  float l[V];
+  load_lane<V, F32>(logits, t * ld, first, n, at.wide, l);
+  const bool two = at.groups > 1 && group_top == 2;
+  float top = 0.0f, sum = 1.0f;
+  if constexpr (SOFTMAX) {
+    if (bias != nullptr || two || !renormalize) {  // the weights of a renormalised choice need no other
+      top = kNone;
+#pragma unroll
+      for (int i = 0; i < V; ++i) top = __builtin_fmaxf(top, l[i]);
+      top = row16_max(top);
+      if (!(top > kNone)) top = 0.0f;  // no expert at all
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += expf(l[i] - top);
+      sum = row16_sum(sum);
+    }
+  }
+  float key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = l[i];
+  if (bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = SOFTMAX ? expf(l[i] - top) / sum : sigmoid(l[i]);
+      const float c = s + (i < n ? bias[first + i] : 0.0f);
+      key[i] = l[i] > kNone && c > kNone ? __builtin_fminf(c, 3.402823466e38f) : kNone;
+    }
+  }
+  bool kept = true;
+  if (at.groups > 1) {
+    float a = kNone, b = kNone;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v = key[i];
+      // without a bias the ranks are logits: a sum of two wants their scores (the softmax's
+      // common denominator changes no order)
+      if (two && bias == nullptr && v > kNone) v = SOFTMAX ? expf(v - top) : sigmoid(v);
+      b = __builtin_amdgcn_fmed3f(a, b, v);  // a >= b: the second largest of the three
+      a = __builtin_fmaxf(a, v);
+    }
+    if (at.lanes > 1) merge_two_dpp<kXor1>(a, b);
+    if (at.lanes > 2) merge_two_dpp<kXor2>(a, b);
+    if (at.lanes > 4) merge_two_dpp<kHalfMirror>(a, b);
+    const double mine = rank_of(group_score(a, b, group_top), group);
+    kept = groups_ahead<1>(mine, at.lanes) < topk_groups;
+  }
+  double v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = rank_of(key[i], first + i);
+  sort8(v);
+  if constexpr (V == 2 * kList) {
+    sort8(v + kList);
+    merge8(v, v + kList);
+  }
+  if (at.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < kList; ++i) v[i] = kept ? v[i] : without_rank(v[i]);
+  }
+  merge_lanes<kXor1>(v);
+  merge_lanes<kXor2>(v);
+  merge_lanes<kHalfMirror>(v);
+  merge_lanes<kMirror>(v);
+  double mine = v[0];  // of choice `sub`
+#pragma unroll
+  for (int i = 1; i < kList; ++i) mine = sub == i ? v[i] : mine;
+  const int32_t id = sub < topk ? expert_of(mine) : -1;
+  const bool chosen = id >= 0;
+  const float cl = chosen ? clean_logit(load_logit<F32>(logits, t * ld + id)) : kNone;
+  float s;
+  if constexpr (SOFTMAX) {
+    if (renormalize) top = row16_max(cl);
+    s = chosen ? expf(cl - top) : 0.0f;
+    if (!renormalize) s = chosen ? s / sum : 0.0f;
+  } else {
+    s = chosen ? sigmoid(cl) : 0.0f;
+  }
+  if (renormalize) {
+    const float z = row16_sum(s);
+    s = z > 0.0f ? s / z : 0.0f;
+  }
+  if (sub < topk && token < T) {
+    ids[t * topk + sub] = id;
+    weights[t * topk + sub] = s * scale;
+  }
+}
+
+// ---- one wavefront per token: expert i * 64 + lane sits in register i of its lane ----
 template <int VPL, bool F32, bool SOFTMAX>
 __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ logits, int64_t ld, int64_t T, int E,
                                                     const float* __restrict__ bias, int groups, int group_size,
@@ -277,13 +489,16 @@ using Int = std::integral_constant<int, V>;
 template <bool V>
 using Bool = std::integral_constant<bool, V>;
 
+// fn(Bool<F32>, Bool<SOFTMAX>)
+template <typename Fn>
+hipError_t by_types(const RouteProblem& p, Fn fn) {
+  if (p.f32) return p.softmax ? fn(Bool<true>{}, Bool<true>{}) : fn(Bool<true>{}, Bool<false>{});
+  return p.softmax ? fn(Bool<false>{}, Bool<true>{}) : fn(Bool<false>{}, Bool<false>{});
+}
 // fn(Int<VPL>, Bool<F32>, Bool<SOFTMAX>) for the registers per lane that E needs.
 template <typename Fn>
 hipError_t by_shape(const RouteProblem& p, Fn fn) {
-  auto types = [&](auto vpl) {
-    if (p.f32) return p.softmax ? fn(vpl, Bool<true>{}, Bool<true>{}) : fn(vpl, Bool<true>{}, Bool<false>{});
-    return p.softmax ? fn(vpl, Bool<false>{}, Bool<true>{}) : fn(vpl, Bool<false>{}, Bool<false>{});
-  };
+  auto types = [&](auto vpl) { return by_types(p, [&](auto f32, auto softmax) { return fn(vpl, f32, softmax); }); };
   if (p.E <= 64) return types(Int<1>{});
   if (p.E <= 128) return types(Int<2>{});
   if (p.E <= 256) return types(Int<4>{});
@@ -295,6 +510,31 @@ hipError_t by_shape(const RouteProblem& p, Fn fn) {
 
 hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, int topk_groups, int group_top,
                         int32_t* ids, float* weights, hipStream_t stream) {
+  // sixteen lanes per token: a group's lanes (a power of two) by groups, up to 16 experts each
+  if (p.topk <= kList && groups <= 16) {
+    RowLayout at;
+    at.lanes = 16;
+    while (16 / at.lanes < groups) at.lanes /= 2;
+    at.groups = groups;
+    at.size = p.E / groups;
+    at.per_lane = (at.size + at.lanes - 1) / at.lanes;
+    const int bytes = p.f32 ? 4 : 2;
+    at.wide = at.size % at.lanes == 0 && at.per_lane * bytes % 16 == 0 && p.ld * bytes % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
+    if (at.per_lane <= 2 * kList)
+      return by_types(p, [&](auto f32, auto softmax) {
+        const dim3 grid((unsigned)((p.T + 3) / 4));
+        if (at.per_lane <= kList)
+          hipLaunchKernelGGL((route_row_kernel<kList, f32.value, softmax.value>), grid, dim3(64), 0, stream, p.logits,
+                             p.ld, p.T, at, bias, topk_groups, group_top, p.topk, (int)p.renormalize, p.scale, ids,
+                             weights);
+        else
+          hipLaunchKernelGGL((route_row_kernel<2 * kList, f32.value, softmax.value>), grid, dim3(64), 0, stream,
+                             p.logits, p.ld, p.T, at, bias, topk_groups, group_top, p.topk, (int)p.renormalize, p.scale,
+                             ids, weights);
+        return hipGetLastError();
+      });
+  }
   return by_shape(p, [&](auto vpl, auto f32, auto softmax) {
     hipLaunchKernelGGL((route_kernel<vpl.value, f32.value, softmax.value>), dim3((unsigned)((p.T + 3) / 4)), dim3(256),
                        0, stream, p.logits, p.ld, p.T, p.E, bias, groups, p.E / groups, topk_groups, group_top, p.topk,

@@ -719,3 +719,5 @@ def test_graph_replays():
 def test_other_device_tensors_are_refused():
     with pytest.raises(ValueError, match="device tensor"):
         F.moe_route_topk(torch.zeros(2, 8, device=DEV), 2, bias=torch.zeros(8))
+    with pytest.raises(ValueError, match="device tensor"):
+        F.moe_route_topk(torch.zeros(2, 8, device=DEV), 2, weights=torch.zeros(2, 2))
