@@ -21,6 +21,7 @@ namespace fp8bs {
 namespace {
 
 constexpr float kNone = -__builtin_inff();  // rank of an expert that cannot be chosen
+constexpr float kMost = 3.402823466e38f;    // the largest finite fp32
 
 template <bool F32>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -30,10 +31,20 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
+// The same bits of every logit above -87 (lower ones score as -87: no two scores under 2e-38
+// rank apart), in seven instructions less: one Newton step on a reciprocal of 1 ulp with two
+// fused multiply-adds rounds 1 / d correctly (Markstein, 1990) for d in [1, 2^126), which a
+// comparison with the division over all of those d confirmed.
+__device__ __forceinline__ float rank_sigmoid(float l) {
+  const float d = 1.0f + expf(-__builtin_fmaxf(l, -87.0f));
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
 // A logit as the operator takes it: NaN and -infinity mean an expert that is not
 // available; +infinity is the largest finite value, so that differences stay numbers.
 __device__ __forceinline__ float clean_logit(float l) {
-  return l > kNone ? __builtin_fminf(l, 3.402823466e38f) : kNone;
+  return l > kNone ? __builtin_fminf(l, kMost) : kNone;
 }
 
 // (a, b) = the two largest of (a, b) and (c, d), a >= b.
@@ -67,11 +78,12 @@ constexpr int kNoneHi = 0xC8078000;  // upper half of about -1e39: below every f
 struct RowLayout {
   int lanes, per_lane;
   int groups, size;
-  bool wide;  // a lane's logits are whole aligned 16-byte words
+  bool wide, wide_bias;  // a lane's logits, its biases, are whole aligned 16-byte words
 };
 
 __device__ __forceinline__ double rank_of(float rank, int expert) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, (double)(rank + 0.0f));  // + 0: -0 ranks as 0
+  // + 0: -0 ranks as 0; an infinite rank ranks as the largest number
+  const uint64_t u = __builtin_bit_cast(uint64_t, (double)__builtin_fminf(rank + 0.0f, kMost));
   const int hi = (int)(u >> 32);
   const uint32_t code = (uint32_t)((expert ^ 1023) ^ ((hi >> 31) & 1023));
   const uint32_t top = (uint32_t)(rank > kNone ? hi : kNoneHi);
@@ -136,9 +148,9 @@ __device__ __forceinline__ int groups_ahead(double mine, int lanes) {
   return n;
 }
 
-// V logits of a lane from expert `first` on, `n` of them there.
+// V values of a lane from expert `first` of a row on, `n` of them there (kNone past them).
 template <int V, bool F32>
-__device__ __forceinline__ void load_lane(const void* logits, int64_t row, int first, int n, bool wide, float* l) {
+__device__ __forceinline__ void load_lane(const void* values, int64_t row, int first, int n, bool wide, float* l) {
 #pragma unroll
   for (int i = 0; i < V; ++i) l[i] = kNone;
   if (wide) {  // uniform
@@ -146,21 +158,19 @@ __device__ __forceinline__ void load_lane(const void* logits, int64_t row, int f
 #pragma unroll
     for (int i = 0; i < V; i += M)
       if (i < n) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(logits) +
+        const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const char*>(values) +
                                                         (row + first + i) * (F32 ? 4 : 2));
         if constexpr (F32) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) l[i + k] = clean_logit(__uint_as_float(v[k]));
+          for (int k = 0; k < 4; ++k) l[i + k] = __uint_as_float(v[k]);
         } else {
           unpack_bf16x8(v, l + i);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) l[i + k] = clean_logit(l[i + k]);
         }
       }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < n) l[i] = clean_logit(load_logit<F32>(logits, row + first + i));
+      if (i < n) l[i] = load_logit<F32>(values, row + first + i);
   }
 }
 
@@ -178,6 +188,8 @@ __global__ __launch_bounds__(64) void route_row_kernel(const void* __restrict__ 
   n = group < at.groups ? (n < at.per_lane ? n : at.per_lane) : 0;
   float l[V];
   load_lane<V, F32>(logits, t * ld, first, n, at.wide, l);
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = clean_logit(l[i]);
   const bool two = at.groups > 1 && group_top == 2;
   float top = 0.0f, sum = 1.0f;
   if constexpr (SOFTMAX) {
@@ -197,11 +209,13 @@ __global__ __launch_bounds__(64) void route_row_kernel(const void* __restrict__ 
 #pragma unroll
   for (int i = 0; i < V; ++i) key[i] = l[i];
   if (bias != nullptr) {
+    float b[V];
+    load_lane<V, true>(bias, 0, first, n, at.wide_bias, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float s = SOFTMAX ? expf(l[i] - top) / sum : sigmoid(l[i]);
-      const float c = s + (i < n ? bias[first + i] : 0.0f);
-      key[i] = l[i] > kNone && c > kNone ? __builtin_fminf(c, 3.402823466e38f) : kNone;
+      const float s = SOFTMAX ? expf(l[i] - top) / sum : rank_sigmoid(l[i]);
+      const float c = s + (l[i] > kNone ? b[i] : kNone);
+      key[i] = c > kNone ? c : kNone;
     }
   }
   bool kept = true;
@@ -212,7 +226,7 @@ __global__ __launch_bounds__(64) void route_row_kernel(const void* __restrict__ 
       float v = key[i];
       // without a bias the ranks are logits: a sum of two wants their scores (the softmax's
       // common denominator changes no order)
-      if (two && bias == nullptr && v > kNone) v = SOFTMAX ? expf(v - top) : sigmoid(v);
+      if (two && bias == nullptr && v > kNone) v = SOFTMAX ? expf(v - top) : rank_sigmoid(v);
       b = __builtin_amdgcn_fmed3f(a, b, v);  // a >= b: the second largest of the three
       a = __builtin_fmaxf(a, v);
     }
@@ -296,7 +310,7 @@ __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ log
     const int e = i * 64 + lane;
     key[i] = l[i];
     if (bias != nullptr && e < E && l[i] > kNone) {
-      const float s = SOFTMAX ? expf(l[i] - top) / sum : sigmoid(l[i]);
+      const float s = SOFTMAX ? expf(l[i] - top) / sum : rank_sigmoid(l[i]);
       const float c = s + bias[e];
       key[i] = c > kNone ? c : kNone;
     }
@@ -313,7 +327,7 @@ __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ log
         float v = of[i] == g ? key[i] : kNone;
         // without a bias the ranks are logits: a sum of two wants their scores (the
         // softmax's common denominator changes no order)
-        if (group_top == 2 && bias == nullptr && v > kNone) v = SOFTMAX ? expf(v - top) : sigmoid(v);
+        if (group_top == 2 && bias == nullptr && v > kNone) v = SOFTMAX ? expf(v - top) : rank_sigmoid(v);
         merge_two(a, b, v, kNone);
       }
       merge_two_dpp<kXor1>(a, b);
@@ -521,6 +535,7 @@ hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, in
     const int bytes = p.f32 ? 4 : 2;
     at.wide = at.size % at.lanes == 0 && at.per_lane * bytes % 16 == 0 && p.ld * bytes % 16 == 0 &&
               reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
+    at.wide_bias = at.size % at.lanes == 0 && at.per_lane % 4 == 0 && reinterpret_cast<uintptr_t>(bias) % 16 == 0;
     if (at.per_lane <= 2 * kList)
       return by_types(p, [&](auto f32, auto softmax) {
         const dim3 grid((unsigned)((p.T + 3) / 4));
