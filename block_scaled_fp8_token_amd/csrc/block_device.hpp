@@ -33,7 +33,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_run(const void* base, u
   void* ptr = reinterpret_cast<void*>(((uint64_t)hi << 32) | lo);
   return __builtin_amdgcn_make_buffer_rsrc(ptr, (short)0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
-constexpr int kStream = 2;  // cache policy of a buffer instruction: streaming
+constexpr int kStream = 2;
 __device__ __forceinline__ u32x4 run_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, kStream));
 }
@@ -100,19 +100,6 @@ __device__ __forceinline__ float wave_max(float v) {
   v = row16_max(v);
   return __builtin_fmaxf(__builtin_fmaxf(read_lane(v, 0), read_lane(v, 16)),
                          __builtin_fmaxf(read_lane(v, 32), read_lane(v, 48)));
-}
-
-// Sum over a workgroup of `waves` wavefronts (at most 16), the same value in every
-// thread.  `part` is sixteen floats of LDS; a caller that reduces again uses another
-// `part` in between (the barrier of that one separates the two uses of this one).
-__device__ __forceinline__ float block_sum(float v, float* part, int waves) {
-  v = wave_sum(v);
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < waves; ++w) s += part[w];
-  return s;
 }
 
 // Two fp32 values as packed bf16, round to nearest even (infinities and NaN kept).

@@ -437,7 +437,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
   }
   const bool chosen = id >= 0;
   const bool dense = SOFTMAX && !renormalize;
-  float l[VPL], top = 0.0f, sum = 1.0f;
+  float l[VPL], top = 0.0f, inv = 0.0f;
   if (dense) {
     top = kNone;
 #pragma unroll
@@ -448,20 +448,20 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
     }
     top = wave_max(top);
     if (!(top > kNone)) top = 0.0f;
-    sum = 0.0f;
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       l[i] = expf(l[i] - top);
       sum += l[i];
     }
     sum = wave_sum(sum);
-    if (!(sum > 0.0f)) sum = 1.0f;  // no expert at all: every share is 0
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // no expert at all: every share is 0
   }
   float g = 0.0f;      // of choice `lane`
   float inner = 0.0f;  // dense: sum_j dw_j p_j
   if (dense) {
     g = dw;
-    inner = wave_sum(chosen ? dw * (expf(cl - top) / sum) : 0.0f);
+    inner = wave_sum(chosen ? dw * (expf(cl - top) * inv) : 0.0f);
   } else {
     float s;
     if constexpr (SOFTMAX) {
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
       const float gj = read_lane(g, j);
       if (ej == e) d += gj;
     }
-    if (dense) d = (l[i] / sum) * (d - inner);
+    if (dense) d = (l[i] * inv) * (d - inner);
     if (e < E) {
       if constexpr (F32)
         static_cast<float*>(d_logits)[t * ld_d + e] = d;

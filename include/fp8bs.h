@@ -334,7 +334,9 @@ int fp8_block_gemm_grouped_masked_preshuffled_cfg(const void* a, const uint32_t*
  * The operators around the experts' products: routing, combine, the norms of the
  * residual stream, and an 8-bit checkpoint of the gated activation, each with its
  * backward pass.  The conventions at the top of this file hold; rows that a call
- * leaves out (padding, pairs without a slot) are neither read nor written.
+ * leaves out (padding, pairs without a slot) are neither read nor written.  Where a call
+ * quantizes "as fp8_quant_group_pack", finite values get the same codes and scales; a value
+ * that is not finite gets the NaN code.
  */
 enum { FP8BS_SIGMOID = 0, FP8BS_SOFTMAX = 1 };
 
@@ -351,7 +353,8 @@ enum { FP8BS_SIGMOID = 0, FP8BS_SOFTMAX = 1 };
  * An expert whose logit is NaN or -infinity, or whose rank is (a NaN bias), is not
  * available; where fewer than topk are, the ids that are left are -1 with weight 0, which
  * every other entry point takes as a pair that goes nowhere.  +infinity counts as the
- * largest finite logit.  All arithmetic is fp32.
+ * largest finite logit.  All arithmetic is fp32; in ranks, sigmoid scores of logits under
+ * -87 (below 2e-38) count as one.
  *   logits   : fp32 (logits_f32 = 1) or bf16 [T][ld], ld >= E; aligned to their type only
  *   bias     : fp32 [E] or NULL
  *   topk_ids : int32 [T][topk] out;  weights : fp32 [T][topk] out

@@ -548,6 +548,34 @@ def test_checkpoint(counts, M, H):
         assert torch.equal(rows, rsf[:, :E * M].t().reshape(E, M, W)[v])
 
 
+def test_checkpoint_of_every_gate():
+    # every finite bf16 pattern as a gate: the same codes as the forward without a checkpoint
+    bits = np.arange(65536, dtype=np.uint32).astype(np.uint16)
+    bits = bits[(bits & 0x7F80) != 0x7F80]
+    gate = torch.from_numpy(bits.view(np.int16)).view(BF).to(DEV).reshape(1, -1, 128)
+    x = torch.cat([gate, torch.ones_like(gate)], -1).contiguous()
+    m = torch.tensor([x.shape[1]], dtype=torch.int32, device=DEV)
+    q, sf, _, _ = F.silu_mul_quant_group_pack_checkpoint(x, m)
+    q2, sf2 = F.silu_mul_quant_group_pack(x, m)
+    assert torch.equal(q, q2) and torch.equal(sf, sf2)
+
+
+def test_values_that_are_not_finite_become_nan_codes():
+    x = torch.randn(1, 3, 512, device=DEV).to(BF)
+    x[0, 1, 5], x[0, 1, 300] = math.nan, math.inf
+    m = torch.tensor([3], dtype=torch.int32, device=DEV)
+    q, _, cq, _ = F.silu_mul_quant_group_pack_checkpoint(x, m)
+    nan = lambda c: c.view(torch.float8_e4m3fn).float().isnan().nonzero().tolist()  # noqa: E731
+    assert nan(cq) == [[0, 1, 5], [0, 1, 300]]
+    assert [0, 1, 5] in nan(q) and [0, 1, 44] in nan(q)
+    w = torch.ones(256, dtype=BF, device=DEV)
+    _, _, q, _ = F.residual_rms_norm(x[0, :, :256].contiguous(), w, out="fp8")
+    assert nan(q)[0][0] == 1 and nan(q)[-1][0] == 1  # row 1 and no other
+    ids, slots = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    q, _, _ = F.moe_combine_backward(x[0, 1:2, :256].contiguous(), x[:, :1, :256].contiguous(), ids, slots, quantize=True)
+    assert nan(q) == [[0, 0, 5]]
+
+
 def checkpoint_of(x, m):
     _, _, cq, csf = F.silu_mul_quant_group_pack_checkpoint(x, m)
     E, M, H2 = x.shape
