@@ -91,9 +91,24 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
-def _launch(name, stream, inputs, *args):
-    """Calls the library on `stream` (None: the current one) once every input is known to lie on
-    the current device (the outputs lie beside an input, see _out)."""
+def _on_stream(stream, fn, *args):
+    """fn(*args) on a stream that the caller names: new outputs come from that stream's memory, and
+    the tensors that the caller passed are kept until its work on them is done."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream == torch.cuda.current_stream():
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        got = fn(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return got
+
+
+def _launch(name, inputs, *args):
+    """Calls the library on the current stream once every input is known to lie on the current
+    device (the outputs lie beside an input, see _out)."""
     dev = inputs[0].get_device()
     for t in inputs:
         if t is not None and t.get_device() != dev:
@@ -102,11 +117,7 @@ def _launch(name, stream, inputs, *args):
         raise ValueError("%s: every tensor must be a device tensor, all on one device" % name)
     if dev != _current_device():
         raise ValueError("%s: the tensors are on cuda:%d, which is not the current device" % (name, dev))
-    if stream is None:
-        stream = _raw_stream(dev)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    st = getattr(_lib, name)(*args, stream)
+    st = getattr(_lib, name)(*args, _raw_stream(dev))
     if st:
         _check(name, st)
 
@@ -120,6 +131,9 @@ def moe_route_topk(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = 
     choice only; groups > 1 restricts the choice to the topk_groups groups of the best score (their best rank,
     or with group_top = 2 the sum of the two best).  Experts with a logit of -inf or NaN are not available;
     ids that are left over are -1 with weight 0."""
+    if stream is not None:
+        return _on_stream(stream, moe_route_topk, logits, topk, bias, groups, topk_groups, group_top, scoring,
+                          renormalize, scale, topk_ids, weights)
     T, E = _2d(logits, "logits")
     pl, ld = _rows(logits, "logits", _FLOAT, T, E)
     if scoring not in _SCORING:
@@ -127,7 +141,7 @@ def moe_route_topk(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = 
     pb = None if bias is None else _whole(bias, "bias", _F32, (E,))
     topk_ids, pi = _out(topk_ids, "topk_ids", _I32, (T, topk), logits)
     weights, pw = _out(weights, "weights", _F32, (T, topk), logits)
-    _launch("moe_route_topk", stream, (logits, bias), pl, logits.dtype == torch.float32, ld, T, E, pb,
+    _launch("moe_route_topk", (logits, bias), pl, logits.dtype == torch.float32, ld, T, E, pb,
             _SCORING[scoring], groups, topk_groups, group_top, topk, bool(renormalize), scale, pi, pw)
     return topk_ids, weights
 
@@ -137,6 +151,9 @@ def moe_route_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, d_weig
                             d_logits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of moe_route_topk's weights with respect to the logits, the choice held fixed: d_weights fp32
     [T, topk] -> d_logits [T, E] of the logits' type.  scoring, renormalize and scale are the forward's."""
+    if stream is not None:
+        return _on_stream(stream, moe_route_topk_backward, logits, topk_ids, d_weights, scoring, renormalize, scale,
+                          d_logits)
     T, E = _2d(logits, "logits")
     pl, ld = _rows(logits, "logits", _FLOAT, T, E)
     topk = _2d(topk_ids, "topk_ids")[1]
@@ -145,7 +162,7 @@ def moe_route_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, d_weig
     pi = _whole(topk_ids, "topk_ids", _I32, (T, topk))
     pw = _whole(d_weights, "d_weights", _F32, (T, topk))
     d_logits, pd, ld_d = _out_rows(d_logits, "d_logits", (logits.dtype,), T, E, logits)
-    _launch("moe_route_topk_backward", stream, (logits, topk_ids, d_weights), pl,
+    _launch("moe_route_topk_backward", (logits, topk_ids, d_weights), pl,
             logits.dtype == torch.float32, ld, T, E, pi, pw, _SCORING[scoring], topk, bool(renormalize), scale, pd, ld_d)
     return d_logits
 
@@ -155,6 +172,8 @@ def moe_combine(y: torch.Tensor, topk_ids: torch.Tensor, slot_of: torch.Tensor, 
     """Experts' rows back to their tokens: out[t] = base[t] + sum_j weights[t, j] * y[topk_ids[t, j], slot_of[t, j]].
     y bf16 [E, M_max, N], topk_ids and slot_of int32 [T, topk] (as fp8_quant_group_pack_to_experts gives them; pairs
     without a row are left out), weights fp32 [T, topk] (None: ones), base bf16 [T, N] -> bf16 [T, N]."""
+    if stream is not None:
+        return _on_stream(stream, moe_combine, y, topk_ids, slot_of, weights, base, out)
     if y.dim() != 3:
         raise ValueError("y must be [E, M_max, N]")
     E, M_max, N = y.shape
@@ -165,7 +184,7 @@ def moe_combine(y: torch.Tensor, topk_ids: torch.Tensor, slot_of: torch.Tensor, 
     pw = None if weights is None else _whole(weights, "weights", _F32, (T, topk))
     pb, ld_b = (None, 0) if base is None else _rows(base, "base", _BF16, T, N)
     out, po, ld_o = _out_rows(out, "out", _BF16, T, N, y)
-    _launch("moe_combine", stream, (y, topk_ids, slot_of, weights, base), py, pi, ps, pw, pb, ld_b, T, topk, E,
+    _launch("moe_combine", (y, topk_ids, slot_of, weights, base), py, pi, ps, pw, pb, ld_b, T, topk, E,
             M_max, N, po, ld_o)
     return out
 
@@ -177,6 +196,9 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, topk_ids: torch.T
     """Gradients of moe_combine for d_out bf16 [T, N]: (d_y bf16 [E, M_max, N], d_weights fp32 [T, topk]), or with
     quantize (q uint8 [E, M_max, N], sf int32 [E, ceil(N/512), M_max], d_weights) in the masked GEMM's layout.
     d_weights is None where weights is.  Rows of no pair are not written.  (d_out is base's gradient as it is.)"""
+    if stream is not None:
+        return _on_stream(stream, moe_combine_backward, d_out, y, topk_ids, slot_of, weights, quantize, d_y, q, sf,
+                          d_weights)
     if y.dim() != 3:
         raise ValueError("y must be [E, M_max, N]")
     E, M_max, N = y.shape
@@ -201,7 +223,7 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, topk_ids: torch.T
         if q is not None or sf is not None:
             raise ValueError("q and sf are written with quantize only")
         d_y, pdy = _out(d_y, "d_y", _BF16, (E, M_max, N), y)
-    _launch("moe_combine_backward", stream, (d_out, y, topk_ids, slot_of, weights), pd, ld_d, py,
+    _launch("moe_combine_backward", (d_out, y, topk_ids, slot_of, weights), pd, ld_d, py,
             pi, ps, pw, T, topk, E, M_max, N, pdy, pq, psf, pdw)
     return (q, sf, d_weights) if quantize else (d_y, d_weights)
 
@@ -227,6 +249,9 @@ def residual_rms_norm(x: torch.Tensor, w_pre: torch.Tensor, y: torch.Tensor | No
     [T, N]; "fp8": q uint8 [T, N] and sf int32 [ceil(N/512), round_up(T, 4)] as fp8_quant_group_pack gives them;
     "both".  Returns (h, z, q, sf), None for what is not asked for.  Without y and with residual_scale 1, h is x itself
     and is not written (pass h to have a copy)."""
+    if stream is not None:
+        return _on_stream(stream, residual_rms_norm, x, w_pre, y, w_post, gate, residual_scale, eps, weight_offset,
+                          out, h, z, q, sf)
     T, N = _2d(x, "x")
     px, ldx = _rows(x, "x", _FLOAT, T, N)
     if out not in _OUT:
@@ -259,7 +284,7 @@ def residual_rms_norm(x: torch.Tensor, w_pre: torch.Tensor, y: torch.Tensor | No
         psf, ld_sf = sf.data_ptr(), sf.stride(0)
     elif q is not None or sf is not None:
         raise ValueError("q and sf are not written with out=%r" % out)
-    _launch("residual_rms_norm", stream, (x, y, w_post, gate, w_pre), px, ldx, x.dtype == torch.float32, py,
+    _launch("residual_rms_norm", (x, y, w_post, gate, w_pre), px, ldx, x.dtype == torch.float32, py,
             ldy, pwp, pg, ld_g, pw, residual_scale, eps, weight_offset, T, N, ph, ldh, pz, ldz, pq, ldq, psf, ld_sf)
     return x if h is None else h, z, q, sf
 
@@ -274,6 +299,9 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
     """Gradients of residual_rms_norm: from d_z bf16 [T, N], the h it returned and (with the residual stream's
     gradient d_h, of h's type) -> (d_x, d_y, d_w_pre, d_w_post, d_gate), None for parts that are not there.  d_x has h's
     type, d_y is bf16, the weights' gradients are fp32 [N]; d_gate is fp32 [N] for a gate [N] and bf16 [T, N] else."""
+    if stream is not None:
+        return _on_stream(stream, residual_rms_norm_backward, d_z, h, w_pre, d_h, y, w_post, gate, residual_scale,
+                          eps, weight_offset, d_x, d_y, d_w_pre, d_w_post, d_gate)
     T, N = _2d(h, "h")
     pz, ld_z = _rows(d_z, "d_z", _BF16, T, N)
     ph, ldh = _rows(h, "h", _FLOAT, T, N)
@@ -298,7 +326,7 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
             d_gate, pdg = _out(d_gate, "d_gate", _F32, (N,), h)
         else:
             d_gate, pdg, ld_dg = _out_rows(d_gate, "d_gate", _BF16, T, N, h)
-    _launch("residual_rms_norm_backward", stream,
+    _launch("residual_rms_norm_backward",
             (d_z, d_h, h, y, w_post, gate, w_pre), pz, ld_z, pdh, ld_dh, ph, ldh,
             h.dtype == torch.float32, py, ldy, pwp, pg, ld_g, pw, residual_scale, eps, weight_offset, T, N, pdx, ld_dx,
             pdy, ld_dy, pdw, pdwp, pdg, ld_dg)
@@ -311,6 +339,8 @@ def silu_mul_quant_group_pack_checkpoint(x: torch.Tensor, masked_m: torch.Tensor
     """silu_mul_quant_group_pack that also keeps gate and up in 8 bits for the backward pass.  x bf16
     [E, M_max, 2H], masked_m int32 [E] -> (q uint8 [E, M_max, H], sf int32 [E, ceil(H/512), M_max], cq uint8
     [E, M_max, 2H], csf int32 [E, 2 * ceil(H/512), M_max]); padded rows are not written."""
+    if stream is not None:
+        return _on_stream(stream, silu_mul_quant_group_pack_checkpoint, x, masked_m, q, sf, cq, csf)
     if x.dim() != 3 or x.shape[2] % 2:
         raise ValueError("x must be [E, M_max, 2H]")
     E, M_max, H2 = x.shape
@@ -321,7 +351,7 @@ def silu_mul_quant_group_pack_checkpoint(x: torch.Tensor, masked_m: torch.Tensor
     sf, psf = _out(sf, "sf", _U32, (E, W, M_max), x)
     cq, pc = _out(cq, "cq", _E4M3, (E, M_max, H2), x)
     csf, pcs = _out(csf, "csf", _U32, (E, 2 * W, M_max), x)
-    _launch("silu_mul_quant_group_pack_checkpoint", stream, (x, masked_m), px, pm, E, M_max, H, pq, psf,
+    _launch("silu_mul_quant_group_pack_checkpoint", (x, masked_m), px, pm, E, M_max, H, pq, psf,
             pc, pcs)
     return q, sf, cq, csf
 
@@ -332,6 +362,8 @@ def silu_mul_backward_from_checkpoint(d_y: torch.Tensor, masked_m: torch.Tensor,
     """Gradient of silu(gate) * up from the 8-bit checkpoint: d_y bf16 [E, M_max, H] -> d_x bf16 [E, M_max, 2H], or
     with quantize (q uint8 [E, M_max, 2H], sf int32 [E, ceil(2H/512), M_max]) in the masked GEMM's layout; padded
     rows are not written."""
+    if stream is not None:
+        return _on_stream(stream, silu_mul_backward_from_checkpoint, d_y, masked_m, cq, csf, quantize, d_x, q, sf)
     if d_y.dim() != 3:
         raise ValueError("d_y must be [E, M_max, H]")
     E, M_max, H = d_y.shape
@@ -350,6 +382,6 @@ def silu_mul_backward_from_checkpoint(d_y: torch.Tensor, masked_m: torch.Tensor,
         if q is not None or sf is not None:
             raise ValueError("q and sf are written with quantize only")
         d_x, px = _out(d_x, "d_x", _BF16, (E, M_max, 2 * H), d_y)
-    _launch("silu_mul_backward_from_checkpoint", stream, (d_y, masked_m, cq, csf), pd, pm, E, M_max, H, pc,
+    _launch("silu_mul_backward_from_checkpoint", (d_y, masked_m, cq, csf), pd, pm, E, M_max, H, pc,
             pcs, px, pq, psf)
     return (q, sf) if quantize else d_x

@@ -28,16 +28,17 @@ __device__ __forceinline__ int64_t pair_row(const int32_t* __restrict__ ids, con
   return (e >= 0 && e < E && s >= 0 && s < M_max) ? (int64_t)e * M_max + s : -1;
 }
 
-// One workgroup per token and 2048 columns: each thread owns eight columns of the
-// output and issues the loads of up to eight pairs before it uses the first.
+// One workgroup per token and tile of columns (equal tiles of at most 2048): each thread
+// owns eight columns of the output and issues the loads of up to eight pairs before it uses
+// the first.
 __global__ __launch_bounds__(256) void combine_kernel(const int32_t* __restrict__ ids,
                                                       const int32_t* __restrict__ slots,
                                                       const float* __restrict__ weights, int topk, int64_t E,
                                                       int64_t M_max, int64_t N, const uint16_t* __restrict__ y,
                                                       const uint16_t* __restrict__ base, int64_t ld_base,
-                                                      uint16_t* __restrict__ out, int64_t ld_out, int64_t tiles) {
-  const int64_t t = (int64_t)blockIdx.x / tiles;
-  const int64_t col = ((int64_t)blockIdx.x - t * tiles) * 2048 + threadIdx.x * 8;
+                                                      uint16_t* __restrict__ out, int64_t ld_out, unsigned tiles) {
+  const int64_t t = blockIdx.x / tiles;
+  const uint32_t col = (blockIdx.x % tiles * blockDim.x + threadIdx.x) * 8;
   if (col >= N) return;
   float acc[8];
 #pragma unroll
@@ -149,23 +150,23 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(
   }
 }
 
+// Threads that take a row of N in `parts` equal parts, eight columns each.
+unsigned threads_of(int64_t N, int64_t parts) { return (unsigned)((N / 8 + 64 * parts - 1) / (64 * parts) * 64); }
+
 }  // namespace
 
 hipError_t launch_combine(const CombineProblem& p, const uint16_t* y, const uint16_t* base, int64_t ld_base,
                           uint16_t* out, int64_t ld_out, hipStream_t stream) {
-  const int64_t tiles = (p.N + 2047) / 2048;
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)(p.T * tiles)), dim3(256), 0, stream, p.ids, p.slots, p.weights,
-                     p.topk, p.E, p.M_max, p.N, y, base, ld_base, out, ld_out, tiles);
+  const unsigned tiles = (unsigned)((p.N / 8 + 255) / 256);
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)(p.T * tiles)), dim3(threads_of(p.N, tiles)), 0, stream, p.ids,
+                     p.slots, p.weights, p.topk, p.E, p.M_max, p.N, y, base, ld_base, out, ld_out, tiles);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_backward(const CombineProblem& p, const uint16_t* d_out, int64_t ld_d, const uint16_t* y,
                                    uint16_t* d_y, uint8_t* q, uint32_t* sf, float* d_weights, hipStream_t stream) {
   const int64_t W = (p.N / 128 + 3) / 4;
-  // chunks of eight columns over the threads with few left over: one pass up to 4096
-  // columns, then as many equal passes as rows need
-  const int64_t chunks = p.N / 8, passes = (chunks + 511) / 512;
-  const unsigned threads = (unsigned)((((chunks + passes - 1) / passes) + 63) / 64 * 64);
+  const unsigned threads = threads_of(p.N, (p.N / 8 + 511) / 512);
   const dim3 grid((unsigned)p.T, (unsigned)((p.topk + kBatch - 1) / kBatch));
   if (q != nullptr)
     hipLaunchKernelGGL(combine_backward_kernel<true>, grid, dim3(threads), 0, stream, p.ids, p.slots, p.weights,

@@ -259,8 +259,11 @@ bool aligned_or_null(const void* p, uintptr_t a) { return p == nullptr || aligne
 bool bad_rows(const void* p, int64_t ld, int64_t N) { return p != nullptr && ld < N; }
 bool misaligned_rows(const void* p, int64_t ld) { return p != nullptr && (!aligned(p, 16) || ld % 8 != 0); }
 
+// Tokens of one call: what keeps every grid under 2^32 threads.
+constexpr int64_t kMostRows = 1 << 22;
+
 int check_route(int64_t ld, int64_t T, int64_t E, int32_t logits_f32, int32_t scoring, int32_t topk) {
-  if (T < 0 || E < 1 || E > fp8bs::kRouteMaxE || ld < E || T > 4 * (int64_t)INT32_MAX) return FP8BS_ERR_SHAPE;
+  if (T < 0 || E < 1 || E > fp8bs::kRouteMaxE || ld < E || T > kMostRows) return FP8BS_ERR_SHAPE;
   if (topk < 1 || topk > fp8bs::kRouteMaxTopk || topk > E) return FP8BS_ERR_SHAPE;
   if ((logits_f32 != 0 && logits_f32 != 1) || (scoring != FP8BS_SIGMOID && scoring != FP8BS_SOFTMAX))
     return FP8BS_ERR_SHAPE;
@@ -285,7 +288,7 @@ fp8bs::RouteProblem route_problem(const void* logits, int32_t logits_f32, int64_
 // Sizes of the combine and its backward pass; 1: nothing to do.
 int check_combine(int64_t T, int32_t topk, int64_t E, int64_t M_max, int64_t N) {
   if (T < 0 || E < 0 || M_max < 0 || N < 0 || N % 8 != 0 || topk < 1 || topk > 64) return FP8BS_ERR_SHAPE;
-  if (T > INT32_MAX || E > INT32_MAX || M_max > INT32_MAX || N > (1 << 30) || T * ((N + 2047) / 2048) > INT32_MAX)
+  if (T > kMostRows || E > INT32_MAX || M_max > INT32_MAX || N > (1 << 20) || T * ((N + 2047) / 2048) > 4 * kMostRows)
     return FP8BS_ERR_SHAPE;
   return T == 0 || N == 0 ? 1 : FP8BS_OK;
 }

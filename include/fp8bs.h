@@ -358,7 +358,7 @@ enum { FP8BS_SIGMOID = 0, FP8BS_SOFTMAX = 1 };
  *   logits   : fp32 (logits_f32 = 1) or bf16 [T][ld], ld >= E; aligned to their type only
  *   bias     : fp32 [E] or NULL
  *   topk_ids : int32 [T][topk] out;  weights : fp32 [T][topk] out
- *   1 <= E <= 1024, 1 <= topk <= 64, groups divides E, groups <= 64,
+ *   T <= 2^22, 1 <= E <= 1024, 1 <= topk <= 64, groups divides E, groups <= 64,
  *   1 <= topk_groups <= groups, topk <= topk_groups * E / groups, group_top <= E / groups.
  * Backward: the choice is held fixed and the bias gets no gradient.  d_logits [T][ld_d]
  * has the type of the logits and is written whole, zeros included.  logits, topk_ids and
@@ -380,7 +380,8 @@ int moe_route_topk_backward(const void* logits, int32_t logits_f32, int64_t ld, 
  *   y         : bf16 [E][M_max][N] (what the masked GEMM wrote)
  *   topk_ids, slot_of : int32 [T][topk];  weights : fp32 [T][topk] or NULL
  *   base      : bf16 [T][ld_base] or NULL;  out : bf16 [T][ld_out]
- *   N % 8 == 0, 1 <= topk <= 64, ld_base and ld_out >= N and % 8 == 0.
+ *   T <= 2^22, N % 8 == 0, N <= 2^20, T * ceil(N/2048) <= 2^24, 1 <= topk <= 64,
+ *   ld_base and ld_out >= N and % 8 == 0.
  * Backward, for every pair that has a row: d_y[e][s] = weights[t][j] * d_out[t], in bf16
  * (d_y [E][M_max][N]) or, with d_y = NULL, as q e4m3 [E][M_max][N] and sf uint32
  * [E][ceil(N/512)][M_max] quantized as fp8_quant_group_pack quantizes the fp32 values

@@ -140,7 +140,8 @@ def test_combine_status():
         return _lib.moe_combine(y, ids, slots, w, base, ld_base, T, topk, E, M, N, out, ld_out, None)
     assert fwd(N=60) == ERR_SHAPE and fwd(topk=0) == ERR_SHAPE and fwd(topk=65) == ERR_SHAPE and fwd(T=-1) == ERR_SHAPE
     assert fwd(ld_out=56) == ERR_SHAPE and fwd(base=B, ld_base=56) == ERR_SHAPE and fwd(E=-1) == ERR_SHAPE
-    assert fwd(T=1 << 33) == ERR_SHAPE
+    assert fwd(T=1 << 33) == ERR_SHAPE and fwd(T=(1 << 22) + 1) == ERR_SHAPE and fwd(N=1 << 21, ld_out=1 << 21) == ERR_SHAPE
+    assert _route(T=(1 << 22) + 1) == ERR_SHAPE
     assert fwd(y=None) == ERR_NULL and fwd(out=None) == ERR_NULL and fwd(slots=None) == ERR_NULL
     assert fwd(y=A + 8) == ERR_ALIGN and fwd(ld_out=68) == ERR_ALIGN and fwd(base=B, ld_base=68) == ERR_ALIGN
     assert fwd(T=0, y=None) == OK and fwd(N=0) == OK

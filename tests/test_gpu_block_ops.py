@@ -709,9 +709,11 @@ def test_on_another_stream_and_again():
         assert torch.equal(a, b)
     # and with the stream as an argument
     ids, w = F.moe_route_topk(s["logits"], 4, scoring="softmax", stream=other)
+    ids3, w3 = F.moe_route_topk(s["logits"], 4, scoring="softmax", stream=other.cuda_stream)  # or its handle
     other.synchronize()
     ids2, w2 = F.moe_route_topk(s["logits"], 4, scoring="softmax")
     assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    assert torch.equal(ids3, ids2) and torch.equal(w3, w2)
 
 
 def test_graph_replays():
