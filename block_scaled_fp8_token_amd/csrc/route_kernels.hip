@@ -7,10 +7,18 @@
 // highest ranks are chosen, ties to the lowest index, and weighted by
 // scale * s, or scale * s / (sum of the chosen s).
 //
-// Two kernels.  route_row_kernel, for up to eight of up to 256 experts: sixteen lanes route
+// Two kernels.  route_row_kernel, for up to eight of up to 512 experts: sixteen lanes route
 // one token, each lane sorts the ranks it holds, and four merges leave the token's eight
 // best in every lane.  route_kernel, for everything else: one wavefront routes one token
 // and takes one maximum per choice.
+//
+// Bound by vector instructions (about 1350 in a wavefront for four tokens; the memory would
+// take 2 us below) and, for few tokens, by the length of their chain.  Measured in a graph,
+// bf16 logits, 16384 tokens, 256 experts: 8 chosen in 4 of 8 groups by biased sigmoid scores
+// 11.3 us, 8 by softmax 7.1 us; 9 chosen, which the second kernel takes, 18 us (it took 36
+// us for the 8 in groups).  512 experts: 8 chosen 15.9 and 10.0 us, 9 chosen 27 us.  One token of
+// 256: 5.6 and 3.6 us.  Backward, softmax not renormalised: 11.1 us, 14.9 us with a memory
+// instruction for every 64 logits and a comparison of every choice with every expert.
 #include <type_traits>
 
 #include "block_device.hpp"
@@ -240,9 +248,10 @@ __global__ __launch_bounds__(64) void route_row_kernel(const void* __restrict__ 
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = rank_of(key[i], first + i);
   sort8(v);
-  if constexpr (V == 2 * kList) {
-    sort8(v + kList);
-    merge8(v, v + kList);
+#pragma unroll
+  for (int i = kList; i < V; i += kList) {
+    sort8(v + i);
+    merge8(v, v + i);
   }
   if (at.groups > 1) {
 #pragma unroll
@@ -407,21 +416,74 @@ __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ log
   }
 }
 
+// The VPL logits of a lane, kept or written as one piece where they are (WIDE: experts
+// lane * VPL .. of a row, aligned to all of them or to 16 bytes), else one by one (experts
+// lane, lane + 64, ..).
+template <int VPL, bool F32, bool WIDE>
+struct LaneRow {
+  static constexpr int kBytes = VPL * (F32 ? 4 : 2);
+  typedef std::conditional_t<F32, float, uint16_t> T;
+  struct alignas(kBytes < 16 ? kBytes : 16) Piece {
+    T v[VPL];
+  };
+  static __device__ __forceinline__ int expert(int lane, int i) { return WIDE ? lane * VPL + i : i * 64 + lane; }
+  static __device__ __forceinline__ void load(const void* row, int lane, int E, float* l) {
+    const T* from = static_cast<const T*>(row);
+    Piece p = {};
+    if constexpr (WIDE) {
+      if (lane * VPL < E) p = *reinterpret_cast<const Piece*>(from + lane * VPL);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (expert(lane, i) < E) p.v[i] = from[expert(lane, i)];
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float v;
+      if constexpr (F32) v = p.v[i];
+      else v = __uint_as_float((uint32_t)p.v[i] << 16);
+      l[i] = expert(lane, i) < E ? clean_logit(v) : kNone;
+    }
+  }
+  static __device__ __forceinline__ void store(void* row, int lane, int E, const float* d) {
+    T* to = static_cast<T*>(row);
+    Piece p;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if constexpr (F32) p.v[i] = d[i];
+      else p.v[i] = (uint16_t)bf16x2_rne(d[i], 0.0f);
+    }
+    if constexpr (WIDE) {
+      if (lane * VPL < E) *reinterpret_cast<Piece*>(to + lane * VPL) = p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (expert(lane, i) < E) to[expert(lane, i)] = p.v[i];
+    }
+  }
+};
+
 // With r_j = s_j / sum of the chosen s and D = sum_j dw_j r_j, the gradient is
 //   renormalised: c r_j (dw_j - D) at the chosen experts, for sigmoid scores times
 //   1 - s_j = sigmoid(-l_j) (the softmax's own sum cancels: it divides every s alike);
 //   else: sigmoid c dw_j s_j (1 - s_j) at the chosen experts, softmax
 //   p_e (c dw_e - c sum_j dw_j p_j) at every expert (dw_e = 0 where not chosen).
-// Every row is written whole, zeros included.
-template <int VPL, bool F32, bool SOFTMAX>
+// Every row is written whole, zeros included.  The value of choice j is written into the
+// register and lane of its expert, both of which the whole wavefront knows.
+template <int VPL, bool F32, bool SOFTMAX, bool WIDE>
 __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restrict__ logits, int64_t ld, int64_t T,
                                                              int E, const int32_t* __restrict__ ids,
                                                              const float* __restrict__ d_weights, int topk,
                                                              int renormalize, float scale, void* __restrict__ d_logits,
                                                              int64_t ld_d) {
+  using Row = LaneRow<VPL, F32, WIDE>;
+  constexpr int kBytes = F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= T) return;
+  const bool dense = SOFTMAX && !renormalize;
+  float l[VPL];
+  if (dense) Row::load(static_cast<const char*>(logits) + t * ld * kBytes, lane, E, l);
   // the chosen experts: lane j holds choice j
   int32_t id = -1;
   float dw = 0.0f, cl = kNone;
@@ -436,16 +498,12 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
     }
   }
   const bool chosen = id >= 0;
-  const bool dense = SOFTMAX && !renormalize;
-  float l[VPL], top = 0.0f, inv = 0.0f;
+  float g = 0.0f;      // of choice `lane`
+  float inner = 0.0f;  // dense: sum_j dw_j p_j
   if (dense) {
-    top = kNone;
+    float top = kNone;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 64 + lane;
-      l[i] = e < E ? clean_logit(load_logit<F32>(logits, t * ld + e)) : kNone;
-      top = __builtin_fmaxf(top, l[i]);
-    }
+    for (int i = 0; i < VPL; ++i) top = __builtin_fmaxf(top, l[i]);
     top = wave_max(top);
     if (!(top > kNone)) top = 0.0f;
     float sum = 0.0f;
@@ -455,11 +513,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
       sum += l[i];
     }
     sum = wave_sum(sum);
-    inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // no expert at all: every share is 0
-  }
-  float g = 0.0f;      // of choice `lane`
-  float inner = 0.0f;  // dense: sum_j dw_j p_j
-  if (dense) {
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;  // no expert at all: every share is 0
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] *= inv;
     g = dw;
     inner = wave_sum(chosen ? dw * (expf(cl - top) * inv) : 0.0f);
   } else {
@@ -479,23 +535,23 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
     }
     if constexpr (!SOFTMAX) g = chosen ? g * sigmoid(-cl) : 0.0f;
   }
+  float d[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 64 + lane;
-    float d = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-      const int32_t ej = __builtin_amdgcn_readlane(id, j);
-      const float gj = read_lane(g, j);
-      if (ej == e) d += gj;
-    }
-    if (dense) d = (l[i] * inv) * (d - inner);
-    if (e < E) {
-      if constexpr (F32)
-        static_cast<float*>(d_logits)[t * ld_d + e] = d;
-      else
-        static_cast<uint16_t*>(d_logits)[t * ld_d + e] = (uint16_t)bf16x2_rne(d, 0.0f);
-    }
+  for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
+  for (int j = 0; j < topk; ++j) {
+    const int e = __builtin_amdgcn_readlane(id, j);
+    if (e < 0) continue;  // uniform, as all of this
+    const float gj = read_lane(g, j);
+    const int at = WIDE ? e % VPL : e >> 6, owner = WIDE ? e / VPL : e & 63;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (at == i) d[i] = lane == owner ? gj : d[i];
   }
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) d[i] = l[i] * (d[i] - inner);
+  }
+  Row::store(static_cast<char*>(d_logits) + t * ld_d * kBytes, lane, E, d);
 }
 
 template <int V>
@@ -524,7 +580,7 @@ hipError_t by_shape(const RouteProblem& p, Fn fn) {
 
 hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, int topk_groups, int group_top,
                         int32_t* ids, float* weights, hipStream_t stream) {
-  // sixteen lanes per token: a group's lanes (a power of two) by groups, up to 16 experts each
+  // sixteen lanes per token: a group's lanes (a power of two) by groups, up to 32 experts each
   if (p.topk <= kList && groups <= 16) {
     RowLayout at;
     at.lanes = 16;
@@ -536,19 +592,17 @@ hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, in
     at.wide = at.size % at.lanes == 0 && at.per_lane * bytes % 16 == 0 && p.ld * bytes % 16 == 0 &&
               reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
     at.wide_bias = at.size % at.lanes == 0 && at.per_lane % 4 == 0 && reinterpret_cast<uintptr_t>(bias) % 16 == 0;
-    if (at.per_lane <= 2 * kList)
+    auto by_lane = [&](auto v) {
       return by_types(p, [&](auto f32, auto softmax) {
-        const dim3 grid((unsigned)((p.T + 3) / 4));
-        if (at.per_lane <= kList)
-          hipLaunchKernelGGL((route_row_kernel<kList, f32.value, softmax.value>), grid, dim3(64), 0, stream, p.logits,
-                             p.ld, p.T, at, bias, topk_groups, group_top, p.topk, (int)p.renormalize, p.scale, ids,
-                             weights);
-        else
-          hipLaunchKernelGGL((route_row_kernel<2 * kList, f32.value, softmax.value>), grid, dim3(64), 0, stream,
-                             p.logits, p.ld, p.T, at, bias, topk_groups, group_top, p.topk, (int)p.renormalize, p.scale,
-                             ids, weights);
+        hipLaunchKernelGGL((route_row_kernel<v.value, f32.value, softmax.value>), dim3((unsigned)((p.T + 3) / 4)),
+                           dim3(64), 0, stream, p.logits, p.ld, p.T, at, bias, topk_groups, group_top, p.topk,
+                           (int)p.renormalize, p.scale, ids, weights);
         return hipGetLastError();
       });
+    };
+    if (at.per_lane <= kList) return by_lane(Int<kList>{});
+    if (at.per_lane <= 2 * kList) return by_lane(Int<2 * kList>{});
+    if (at.per_lane <= 4 * kList) return by_lane(Int<4 * kList>{});
   }
   return by_shape(p, [&](auto vpl, auto f32, auto softmax) {
     hipLaunchKernelGGL((route_kernel<vpl.value, f32.value, softmax.value>), dim3((unsigned)((p.T + 3) / 4)), dim3(256),
@@ -561,10 +615,18 @@ hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, in
 hipError_t launch_route_backward(const RouteProblem& p, const int32_t* ids, const float* d_weights, void* d_logits,
                                  int64_t ld_d, hipStream_t stream) {
   return by_shape(p, [&](auto vpl, auto f32, auto softmax) {
-    hipLaunchKernelGGL((route_backward_kernel<vpl.value, f32.value, softmax.value>), dim3((unsigned)((p.T + 3) / 4)),
-                       dim3(256), 0, stream, p.logits, p.ld, p.T, p.E, ids, d_weights, p.topk, (int)p.renormalize,
-                       p.scale, d_logits, ld_d);
-    return hipGetLastError();
+    const uintptr_t piece = vpl.value * (p.f32 ? 4 : 2), align = piece < 16 ? piece : 16;
+    const int64_t row = p.f32 ? 4 : 2;
+    const bool wide = p.E % vpl.value == 0 && p.ld * row % align == 0 && ld_d * row % align == 0 &&
+                      reinterpret_cast<uintptr_t>(p.logits) % align == 0 &&
+                      reinterpret_cast<uintptr_t>(d_logits) % align == 0;
+    auto launch = [&](auto w) {
+      hipLaunchKernelGGL((route_backward_kernel<vpl.value, f32.value, softmax.value, w.value>),
+                         dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, stream, p.logits, p.ld, p.T, p.E, ids,
+                         d_weights, p.topk, (int)p.renormalize, p.scale, d_logits, ld_d);
+      return hipGetLastError();
+    };
+    return wide ? launch(Bool<true>{}) : launch(Bool<false>{});
   });
 }
 

@@ -362,7 +362,7 @@ enum { FP8BS_SIGMOID = 0, FP8BS_SOFTMAX = 1 };
  *   1 <= topk_groups <= groups, topk <= topk_groups * E / groups, group_top <= E / groups.
  * Backward: the choice is held fixed and the bias gets no gradient.  d_logits [T][ld_d]
  * has the type of the logits and is written whole, zeros included.  logits, topk_ids and
- * the options are the forward's; an id of -1 takes no part.
+ * the options are the forward's; an id of -1 takes no part; no id may stand twice in a row.
  */
 int moe_route_topk(const void* logits, int32_t logits_f32, int64_t ld, int64_t T, int64_t E, const float* bias,
                    int32_t scoring, int32_t groups, int32_t topk_groups, int32_t group_top, int32_t topk,

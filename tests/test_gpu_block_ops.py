@@ -72,6 +72,9 @@ ROUTES = [  # T, E, topk, groups, topk_groups, group_top, scoring, bias, dtype
     (6, 513, 3, 1, 1, 1, "sigmoid", True, torch.float32),
     (4, 1024, 64, 64, 8, 2, "sigmoid", True, torch.float32),
     (7, 384, 8, 1, 1, 1, "sigmoid", True, torch.float32),
+    (5, 448, 7, 16, 5, 2, "sigmoid", True, torch.float32),
+    (6, 512, 8, 1, 1, 1, "softmax", False, BF),
+    (9, 40, 9, 1, 1, 1, "softmax", False, torch.float32),
 ]
 
 
