@@ -251,9 +251,9 @@ struct NormSums {
   float *pre, *post, *gate;
 };
 
-// Registers: with one chunk per thread (AHEAD) the row and the weights stay in registers
-// and the next row is loaded while this one is worked on.  With two there is no room: each
-// phase loads what it needs, which the phases after the first find in the L2 cache.
+// Registers: a row stays in them from its loads to its last store.  With one chunk per
+// thread (AHEAD) so do the weights, and the next row is loaded while this one is worked on;
+// with two there is room for neither.
 template <bool F32, bool FULL, int CH>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, NormGradients g, NormSums sums) {
   constexpr bool AHEAD = CH == 1;
@@ -304,19 +304,25 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
       unpack_bf16x8(col < p.N ? load_weights(from, col) : none, w);
     }
   };
-  using Row = GradRow<F32, FULL>;
-  // the row of chunk c, at the start of each phase
-  auto row_of = [&](int c, int64_t r, Row& cur) {
-    if constexpr (AHEAD) {  // packed again, not unpacked values of the phase before
-      for (u32x4& v : cur.h.v) keep_packed(v);
-      keep_packed(cur.d_z);
-      keep_packed(cur.y);
-      for (u32x4& k : kept) keep_packed(k);
-    } else {
-      load_row(p, g, r, (c * blockDim.x + threadIdx.x) * 8, true, cur);
-    }
+  struct Row {
+    GradRow<F32, FULL> c[CH];
   };
-  auto gates = [&](int c, const Row& cur, float* w) {
+  auto load = [&](int64_t r, bool there, Row& row) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) load_row(p, g, r, (c * blockDim.x + threadIdx.x) * 8, there, row.c[c]);
+  };
+  // chunk c of the row, at the start of each phase: packed again, not unpacked values of the
+  // phase before
+  auto chunk_of = [&](int c, Row& row) -> GradRow<F32, FULL>& {
+    GradRow<F32, FULL>& cur = row.c[c];
+    for (u32x4& v : cur.h.v) keep_packed(v);
+    keep_packed(cur.d_z);
+    keep_packed(cur.y);
+    if constexpr (AHEAD)
+      for (u32x4& k : kept) keep_packed(k);
+    return cur;
+  };
+  auto gates = [&](int c, const GradRow<F32, FULL>& cur, float* w) {
     if constexpr (FULL) unpack_bf16x8(cur.gate, w);
     else weights(2, c, w);
   };
@@ -324,18 +330,17 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
   int64_t r = blockIdx.x;  // grid <= T: every workgroup has a row
   // one row; AHEAD: issue the loads of the workgroup's next one first.  The loop alternates
   // two register sets: a copy would wait for the loads in flight.
-  auto work = [&](Row& cur, Row& next) -> bool {
+  auto work = [&](Row& row, Row& next) -> bool {
     const int64_t now = r;
     r += gridDim.x;
     const bool more = r < p.T;
-    if constexpr (AHEAD) {
-      load_row(p, g, r, threadIdx.x * 8, more, next);
-      __builtin_amdgcn_sched_barrier(0);  // those loads go out before this row is worked on
-    }
+    if constexpr (AHEAD) load(r, more, next);
+    else load(now, true, row);
+    __builtin_amdgcn_sched_barrier(0);  // those loads go out before this row is worked on
     float ss = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      row_of(c, now, cur);
+      GradRow<F32, FULL>& cur = chunk_of(c, row);
       float h[8], u[8], w[8];
       unpack_raw<F32>(cur.h, h);
       unpack_bf16x8(cur.d_z, u);
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
-      row_of(c, now, cur);
+      GradRow<F32, FULL>& cur = chunk_of(c, row);
       float h[8], u[8], w[8], dx[8], t[8];
       unpack_raw<F32>(cur.h, h);
       unpack_bf16x8(cur.d_z, u);
@@ -396,7 +401,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
-      row_of(c, now, cur);
+      GradRow<F32, FULL>& cur = chunk_of(c, row);
       float y[8], w[8], gt[8], dy[8], dg[8], t[8];
       unpack_bf16x8(cur.y, y);
 #pragma unroll
@@ -426,7 +431,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
     return more;
   };
   Row a, b;
-  if constexpr (AHEAD) load_row(p, g, r, threadIdx.x * 8, true, a);
+  if constexpr (AHEAD) load(r, true, a);
   while (work(a, b) && work(b, a)) {
   }
 #pragma unroll
@@ -483,12 +488,15 @@ unsigned threads_for(int64_t N, int ch) { return (unsigned)(64 * ((N / 8 + 64 * 
 // Chunks per thread: rows of up to 1024 threads' one chunk, else two.
 int chunks_for(int64_t N) { return N <= 8192 ? 1 : 2; }
 
-// Workgroups of the backward pass: as many as fit a compute unit's registers (16
-// wavefronts), four at the most, as each writes one row of partial sums.
+// Workgroups of the backward pass: what a compute unit's registers hold (sixteen
+// wavefronts), but at least eight rows for each past one workgroup a compute unit, as each
+// writes a row of partial sums (4096 x 2048: 31.5 us with 512 workgroups, 36 with 1024 or
+// 256; 65536 x 512: 103 us with 4096, 176 with 512).
 int backward_blocks(const NormProblem& p) {
-  const int per_cu = 1024 / (int)threads_for(p.N, chunks_for(p.N));
-  const int64_t fit = (int64_t)kCUs * (per_cu < 4 ? per_cu : 4);
-  return (int)(p.T < fit ? p.T : fit);
+  const int64_t fit = (int64_t)kCUs * (1024 / threads_for(p.N, chunks_for(p.N)));
+  const int64_t few = p.T < kCUs ? p.T : kCUs, eight = p.T / 8;
+  const int64_t want = eight > few ? eight : few;
+  return (int)(want < fit ? want : fit);
 }
 
 template <bool V>

@@ -413,7 +413,7 @@ int moe_combine_backward(const void* d_out, int64_t ld_d, const void* y, const i
  * d_w_pre and d_w_post (fp32 [N]) and d_gate (fp32 [N] if ld_gate = 0, else bf16
  * [T][ld_dgate]).  Those of parts that the forward has not are NULL.  The sums over the tokens
  * are taken in a fixed order: equal calls give equal bits.  Their partial sums (at most
- * 12 * 256 * N bytes) go to the library's per-(device, stream) workspace (FP8BS_ERR_ALLOC if
+ * 52 MB) go to the library's per-(device, stream) workspace (FP8BS_ERR_ALLOC if
  * it has to grow during HIP graph capture).  T == 0 sets the weights' gradients to zero.
  */
 int residual_rms_norm(const void* x, int64_t ldx, int32_t residual_f32, const void* y, int64_t ldy, const void* w_post,
