@@ -13,10 +13,12 @@
 // worked on.
 //
 // Measured: forward, 8192 x 7168 from bf16 with both norms and a shared gate to a bf16
-// stream and codes, 75 us, 411 MB, 5.5 TB/s (115 us with a workgroup per row and x loaded
-// after the first reduction).  Backward, 4097 x 7168 with an fp32 stream, 104 us, 528 MB,
-// 5.1 TB/s, and 5.4 us for the sums over the workgroups (154 us in all without the loads
-// ahead, with 134 of it where all three sums stayed in registers and spilled).
+// stream and codes, 73 us, 411 MB, 5.6 TB/s (a copy of 400 MB reaches 5.4): 115 us with a
+// workgroup per row and x loaded after the first reduction, 83 us with the next row's loads
+// ahead, 76 us with those loads and the stores free of branches, 73 us with the weights
+// unpacked once.  Backward, 4097 x 7168 with an fp32 stream, 104 us, 528 MB and 22 MB of
+// partial sums, 5.3 TB/s, and 5.3 us for the sums over the workgroups (154 us in all without the
+// loads ahead, 139 where all three sums stayed in registers and spilled).
 #include <type_traits>
 
 #include "block_device.hpp"
@@ -78,8 +80,8 @@ __device__ __forceinline__ u32x4 load_weights(const uint16_t* w, uint32_t col) {
   return *reinterpret_cast<const u32x4*>(w + col);
 }
 
-// Keeps a register's contents from being known across loop trips, so that weights stay
-// packed in registers instead of being unpacked to twice as many outside the loop.
+// Keeps the compiler from knowing a register's contents, so that a row stays packed between
+// the phases that unpack it instead of being kept unpacked in twice as many registers.
 __device__ __forceinline__ void keep_packed(u32x4& v) { asm volatile("" : "+v"(v)); }
 
 // One row as loaded, the chunks of one thread.  FULL: a gate of its own for every token.
@@ -88,6 +90,15 @@ struct NormRow {
   Raw<F32> x[CH];
   u32x4 y[CH], gate[FULL ? CH : 1];
 };
+
+// 1 / sqrt(mean + eps) of a sum of squares over n (1 / n as a sum of two fp32).  One Newton
+// step on the 1 ulp of rsqrtf, as an error here is one of the whole row and moves its codes; a
+// mean of 0 or past fp32 keeps rsqrtf's answer.
+__device__ __forceinline__ float inverse_rms(float sum, float inv_n, float inv_n_lo, float eps) {
+  const float m = __builtin_fmaf(sum, inv_n, sum * inv_n_lo) + eps, r = rsqrtf(m);
+  const float e = __builtin_fmaf(-(m * r), r, 1.0f);
+  return __builtin_fabsf(e) < 1.0f ? __builtin_fmaf(0.5f * r, e, r) : r;
+}
 
 // Sum over a workgroup of at most sixteen wavefronts, the same value in every thread: each
 // lane takes one wavefront's sum and the sixteen lanes of a row add theirs.  `part` is
@@ -109,20 +120,28 @@ __global__ __launch_bounds__(1024) void norm_kernel(
   __shared__ float part[2][16];
   const int waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const float inv_n = 1.0f / (float)p.N;
-  const u32x4 none = {0u, 0u, 0u, 0u};
+  const float inv_n = 1.0f / (float)p.N, inv_n_lo = __builtin_fmaf(-inv_n, (float)p.N, 1.0f) * inv_n;
   if (threadIdx.x < 32) part[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
   __syncthreads();
   int turn = 0;  // of the halves of `part`: consecutive sums use different ones
-  u32x4 w_post[CH], w_pre[CH], gate[CH];
+  // weights of the columns, in fp32: the branch's (w_post + offset, times a shared gate), z's
+  float w_branch[CH][8], w_z[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
-    w_post[c] = w_pre[c] = gate[c] = none;
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w_branch[c][i] = g[i] = w_z[c][i] = 1.0f;
     if (col < p.N) {
-      w_pre[c] = load_weights(p.w_pre, col);
-      if (p.w_post != nullptr) w_post[c] = load_weights(p.w_post, col);
-      if (!FULL && p.gate != nullptr) gate[c] = load_weights(p.gate, col);
+      unpack_bf16x8(load_weights(p.w_pre, col), w_z[c]);
+      if (p.w_post != nullptr) unpack_bf16x8(load_weights(p.w_post, col), w_branch[c]);
+      if (!FULL && p.gate != nullptr) unpack_bf16x8(load_weights(p.gate, col), g);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (p.w_post != nullptr) w_branch[c][i] += p.offset;
+      w_branch[c][i] *= g[i];
+      w_z[c][i] += p.offset;
     }
   }
   using Row = NormRow<F32, FULL, CH>;
@@ -149,48 +168,41 @@ __global__ __launch_bounds__(1024) void norm_kernel(
     float ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      keep_packed(w_post[c]);
-      keep_packed(w_pre[c]);
-      keep_packed(gate[c]);
       unpack_bf16x8(cur.y[c], v[c]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[c][i], v[c][i], ss);
     }
     float inv = 1.0f;
-    if (p.w_post != nullptr) inv = rsqrtf(block_sum(ss, part[turn ^= 1], waves) * inv_n + p.eps);
+    if (p.w_post != nullptr) inv = inverse_rms(block_sum(ss, part[turn ^= 1], waves), inv_n, inv_n_lo, p.eps);
     const auto hs = row_run(h, ldh, now, p.N, true);
     ss = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
-      float w[8];
-      if (p.w_post != nullptr) {
-        unpack_bf16x8(w_post[c], w);
+      float x8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] *= inv * (w[i] + p.offset);
-      }
-      if (p.gate != nullptr) {
-        unpack_bf16x8(FULL ? cur.gate[FULL ? c : 0] : gate[c], w);
+      for (int i = 0; i < 8; ++i) v[c][i] *= inv * w_branch[c][i];
+      if constexpr (FULL) {
+        float g[8];
+        unpack_bf16x8(cur.gate[c], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] *= w[i];
+        for (int i = 0; i < 8; ++i) v[c][i] *= g[i];
       }
-      unpack_raw<F32>(cur.x[c], w);
+      unpack_raw<F32>(cur.x[c], x8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[c][i] = __builtin_fmaf(p.residual_scale, w[i], v[c][i]);
+        v[c][i] = __builtin_fmaf(p.residual_scale, x8[i], v[c][i]);
         ss = __builtin_fmaf(v[c][i], v[c][i], ss);
       }
       store8<F32>(hs, col, v[c]);
     }
-    inv = rsqrtf(block_sum(ss, part[turn ^= 1], waves) * inv_n + p.eps);
+    inv = inverse_rms(block_sum(ss, part[turn ^= 1], waves), inv_n, inv_n_lo, p.eps);
     const auto zs = row_run(z, ldz, now, p.N, true);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
-      float w[8];
-      unpack_bf16x8(w_pre[c], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] *= inv * (w[i] + p.offset);
+      for (int i = 0; i < 8; ++i) v[c][i] *= inv * w_z[c][i];
       store8<false>(zs, col, v[c]);
       if constexpr (QUANT) {
         const uint32_t byte = group_byte(v[c]);
@@ -259,14 +271,14 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
   constexpr bool AHEAD = CH == 1;
   __shared__ float2 part[2][16];
   const int waves = blockDim.x >> 6;
-  const float inv_n = 1.0f / (float)p.N;
+  const float inv_n = 1.0f / (float)p.N, inv_n_lo = __builtin_fmaf(-inv_n, (float)p.N, 1.0f) * inv_n;
   const u32x4 none = {0u, 0u, 0u, 0u};
   // sums of d_w_pre and d_w_post: four floats of a thread per entry, [2][CH][2][blockDim]
   extern __shared__ u32x4 lds_sums[];
   float s_gate[CH][8];
   if (threadIdx.x < 32) part[threadIdx.x >> 4][threadIdx.x & 15] = make_float2(0.0f, 0.0f);
   __syncthreads();
-  u32x4 kept[3] = {none, none, none};  // AHEAD: w_pre, w_post, a gate shared by the tokens
+  float kept[3][8] = {};  // AHEAD: w_pre + offset, w_post + offset, a gate shared by the tokens
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -289,19 +301,28 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
   if constexpr (AHEAD) {
     const uint32_t col = threadIdx.x * 8;
     if (col < p.N) {
-      kept[0] = load_weights(p.w_pre, col);
-      if (p.w_post != nullptr) kept[1] = load_weights(p.w_post, col);
-      if (!FULL && p.gate != nullptr) kept[2] = load_weights(p.gate, col);
+      unpack_bf16x8(load_weights(p.w_pre, col), kept[0]);
+      if (p.w_post != nullptr) unpack_bf16x8(load_weights(p.w_post, col), kept[1]);
+      if (!FULL && p.gate != nullptr) unpack_bf16x8(load_weights(p.gate, col), kept[2]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      kept[0][i] += p.offset;
+      kept[1][i] += p.offset;
     }
   }
-  // eight of w_pre (which = 0), w_post (1) or a shared gate (2)
+  // eight of w_pre + offset (which = 0), w_post + offset (1) or a shared gate (2)
   auto weights = [&](int which, int c, float* w) {
     if constexpr (AHEAD) {
-      unpack_bf16x8(kept[which], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = kept[which][i];
     } else {
       const uint32_t col = (c * blockDim.x + threadIdx.x) * 8;
       const uint16_t* from = which == 0 ? p.w_pre : (which == 1 ? p.w_post : p.gate);
       unpack_bf16x8(col < p.N ? load_weights(from, col) : none, w);
+      if (which < 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] += p.offset;
     }
   };
   struct Row {
@@ -318,8 +339,6 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
     for (u32x4& v : cur.h.v) keep_packed(v);
     keep_packed(cur.d_z);
     keep_packed(cur.y);
-    if constexpr (AHEAD)
-      for (u32x4& k : kept) keep_packed(k);
     return cur;
   };
   auto gates = [&](int c, const GradRow<F32, FULL>& cur, float* w) {
@@ -348,11 +367,11 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss = __builtin_fmaf(h[i], h[i], ss);
-        dot = __builtin_fmaf(u[i] * (w[i] + p.offset), h[i], dot);
+        dot = __builtin_fmaf(u[i] * w[i], h[i], dot);
       }
     }
     block_sum2(ss, dot, part[turn ^= 1], waves);
-    const float rh = rsqrtf(ss * inv_n + p.eps);
+    const float rh = inverse_rms(ss, inv_n, inv_n_lo, p.eps);
     const float mean = dot * rh * inv_n;  // of u hh
     float d[CH][8];                       // dh
     float ss_y = 0.0f, dot_y = 0.0f;
@@ -369,7 +388,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
       for (int i = 0; i < 8; ++i) {
         const float hh = h[i] * rh;
         t[i] = u[i] * hh;
-        d[c][i] += rh * (u[i] * (w[i] + p.offset) - hh * mean);
+        d[c][i] += rh * (u[i] * w[i] - hh * mean);
         dx[i] = p.residual_scale * d[c][i];
       }
       add_sum(0, c, t);
@@ -378,7 +397,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
         weights(1, c, w);
         unpack_bf16x8(cur.y, h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * (w[i] + p.offset);
+        for (int i = 0; i < 8; ++i) u[i] = d[c][i] * w[i];
         if (p.gate != nullptr) {
           gates(c, cur, w);
 #pragma unroll
@@ -395,7 +414,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
     float ry = 1.0f, mean_y = 0.0f;
     if (p.w_post != nullptr) {
       block_sum2(ss_y, dot_y, part[turn ^= 1], waves);
-      ry = rsqrtf(ss_y * inv_n + p.eps);
+      ry = inverse_rms(ss_y, inv_n, inv_n_lo, p.eps);
       mean_y = dot_y * ry * inv_n;
     }
 #pragma unroll
@@ -409,8 +428,6 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormProblem p, Norm
       if (p.gate != nullptr) gates(c, cur, gt);
       if (p.w_post != nullptr) {
         weights(1, c, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] += p.offset;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -522,9 +539,9 @@ hipError_t launch_norm(const NormProblem& p, const void* x, int64_t ldx, void* h
     using S = Stream<f32.value>;
     auto launch = [&](auto quant) {
       const unsigned threads = threads_for(p.N, ch.value);
-      // sixteen wavefronts on each compute unit (8192 x 7168: 75 us with one workgroup of
-      // fourteen there, 78 with two, 121 with a workgroup for every row; 85 where each had a
-      // contiguous run of the rows)
+      // sixteen wavefronts on each compute unit (8192 x 7168: 79 us with one workgroup of
+      // fourteen there, 82 with two, 121 with a workgroup for every row, before the last steps;
+      // 85 where each had a contiguous run of the rows)
       const int64_t fit = (int64_t)kCUs * (1024 / threads);
       hipLaunchKernelGGL((norm_kernel<f32.value, full.value, quant.value, ch.value>),
                          dim3((unsigned)(p.T < fit ? p.T : fit)), dim3(threads), 0, stream, p,
