@@ -33,7 +33,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_run(const void* base, u
   void* ptr = reinterpret_cast<void*>(((uint64_t)hi << 32) | lo);
   return __builtin_amdgcn_make_buffer_rsrc(ptr, (short)0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
-constexpr int kStream = 2;
+constexpr int kStream = 2;  // cache policy of a buffer instruction: streaming
 __device__ __forceinline__ u32x4 run_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, kStream));
 }

@@ -6,7 +6,8 @@
 // activations to keep until the backward pass.
 // Backward, from the checkpoint: with s = sigmoid(gate),
 //   d_gate = d_y up s (1 + gate (1 - s)),   d_up = d_y gate s
-// in bf16, or quantized for the product that takes the gradient on.
+// in fp32, rounded once: to bf16, or to e4m3 for the masked GEMM that takes the gradient on.
+// The checkpoint's own rounding (at most 2^-4 of a value) is what half the memory costs.
 //
 // Streams bound by memory.  One wavefront takes one (row, 512 columns of H) unit: eight
 // columns of gate and of up per lane, sixteen lanes per quantization group, no LDS for

@@ -73,9 +73,11 @@ __global__ __launch_bounds__(256) void combine_kernel(const int32_t* __restrict_
 // One workgroup per token (and batch of pairs): each thread reads eight columns of d_out
 // once, issues the loads of the same columns of up to eight pairs' rows of y, and writes
 // those pairs' rows of d_y (or their codes).  The weights' gradients stay in registers
-// until the row ends, so a batch costs one barrier.
+// until the row ends, so a batch costs one barrier.  A row of 7168 in two passes of 448
+// threads takes 74 us for 2048 tokens of 8 pairs, as it does in four of 256 or seven of 128;
+// in one of 896 it takes 84.
 //
-// Codes: the group's largest |w d| is |w| times its largest |d| (rounding is monotonic), so
+// Codes (e4m3, since the masked GEMM that takes the gradient on reads nothing wider): the group's largest |w d| is |w| times its largest |d| (rounding is monotonic), so
 // the reduction over the group is made once for all pairs.
 template <bool QUANT>
 __global__ __launch_bounds__(512) void combine_backward_kernel(

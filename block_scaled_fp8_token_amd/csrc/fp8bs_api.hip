@@ -770,6 +770,7 @@ int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, 
     float* sums[3] = {d_w_pre, d_w_post, ld_gate == 0 ? static_cast<float*>(d_gate) : nullptr};
     for (float* s : sums) {
       if (s == nullptr) continue;
+      if (!aligned(s, 16)) return FP8BS_ERR_ALIGN;
       hipError_t e = zero_words(s, (size_t)N * sizeof(float), static_cast<hipStream_t>(stream));
       if (e != hipSuccess) return fail_hip(e);
     }

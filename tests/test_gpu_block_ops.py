@@ -142,6 +142,23 @@ def test_route_extreme_logits():
     assert F.moe_route_topk(l, 3, bias=b, scoring="sigmoid")[0].tolist() == [[0, 3, -1]]
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [2, 9])  # either kernel
+def test_route_masks_of_the_lowest_value(scoring, dtype, k):
+    low = torch.finfo(dtype).min
+    l = torch.full((3, 32), low, dtype=dtype, device=DEV)  # finite: every expert is available
+    l[1, 7] = 1.0
+    l[2, 4], l[2, 9] = torch.finfo(dtype).max, 0.0
+    for renormalize in (True, False):
+        ids, w = F.moe_route_topk(l, k, scoring=scoring, renormalize=renormalize)
+        want = [top + [e for e in range(32) if e not in top] for top in ([], [7], [4, 9])]
+        assert ids.tolist() == [row[:k] for row in want]
+        assert w.isfinite().all()
+        assert float(w[1, 0]) == pytest.approx(1.0 if renormalize or scoring == "softmax" else 1 / (1 + math.exp(-1)))
+        assert not w[1, 1:].any()  # what a mask of the lowest value leaves has no weight
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 @pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("T,E,k,dtype", [(1, 1, 1, torch.float32), (5, 60, 6, BF), (9, 160, 2, torch.float32),
