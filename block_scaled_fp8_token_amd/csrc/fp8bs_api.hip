@@ -66,22 +66,27 @@ hipError_t zero_words(void* p, size_t bytes, hipStream_t stream) {
 // of the call in flight on that stream, which every split overwrites before they
 // are read.  A buffer that is outgrown is kept, never freed: a HIP graph captured
 // earlier on the stream still launches kernels that use it.
+// A call holds the buffer's mutex until its last launch that uses it: of two host threads
+// that call on one stream, neither puts a launch between two launches of the other's call.
 struct Workspace {
+  std::mutex mu;
   void* ptr = nullptr;
   size_t bytes = 0;
   std::vector<void*> retired;
 };
 
-int get_workspace(size_t need, hipStream_t stream, void** out) {
+int get_workspace(size_t need, hipStream_t stream, void** out, std::unique_lock<std::mutex>* held) {
   static std::mutex mu;
-  static std::map<std::pair<int, uintptr_t>, Workspace> pool;
+  static std::map<std::pair<int, uintptr_t>, Workspace> pool;  // entries stay where they are
   *out = nullptr;
   if (need == 0) return FP8BS_OK;
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail_hip(e);
-  std::lock_guard<std::mutex> lk(mu);
+  std::unique_lock<std::mutex> lk(mu);
   Workspace& w = pool[std::make_pair(dev, reinterpret_cast<uintptr_t>(stream))];
+  lk.unlock();  // a call on another stream does not wait for this one's launches
+  *held = std::unique_lock<std::mutex>(w.mu);
   if (w.bytes >= need) {
     *out = w.ptr;
     return FP8BS_OK;
@@ -146,8 +151,9 @@ int static_scratch(hipStream_t stream, void** out) {
 int run_gemm(const fp8bs::GemmProblem& prob, const fp8bs::GemmConfig& cfg, hipStream_t stream) {
   if (cfg.kernel < 0) return FP8BS_ERR_SHAPE;  // no table entry takes this problem
   void* ws = nullptr;
+  std::unique_lock<std::mutex> held;
   const size_t need = fp8bs::gemm_workspace_bytes(prob, cfg);
-  int st = get_workspace(need, stream, &ws);
+  int st = get_workspace(need, stream, &ws, &held);
   if (st != FP8BS_OK) return st;
   hipError_t e = fp8bs::launch_gemm(prob, cfg, ws, stream);
   return e == hipSuccess ? FP8BS_OK : fail_hip(e);
@@ -411,8 +417,9 @@ int fp8_quant_group_pack_to_experts(const void* x, int64_t ldx, int64_t T, int64
   // pair ranks and per-chunk counts live in the stream's workspace past the counters
   const size_t off = fp8bs::gemm_workspace_zeroed_prefix();
   void* ws = nullptr;
+  std::unique_lock<std::mutex> held;
   st = get_workspace(off + fp8bs::quant_to_experts_scratch_bytes(T, topk, E), static_cast<hipStream_t>(stream),
-                     &ws);
+                     &ws, &held);
   if (st != FP8BS_OK) return st;
   hipError_t e = fp8bs::launch_quant_to_experts(static_cast<const uint16_t*>(x), ldx, T, K, topk_ids, topk, E,
                                                 M_max, static_cast<uint8_t*>(q), sf, masked_m, slot_of,
@@ -795,7 +802,8 @@ int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, 
   // partial sums live in the stream's workspace past the split-K arrival counters
   const size_t off = fp8bs::gemm_workspace_zeroed_prefix();
   void* ws = nullptr;
-  st = get_workspace(off + fp8bs::norm_backward_scratch_bytes(p), static_cast<hipStream_t>(stream), &ws);
+  std::unique_lock<std::mutex> held;
+  st = get_workspace(off + fp8bs::norm_backward_scratch_bytes(p), static_cast<hipStream_t>(stream), &ws, &held);
   if (st != FP8BS_OK) return st;
   hipError_t e = fp8bs::launch_norm_backward(p, g, reinterpret_cast<float*>(static_cast<char*>(ws) + off),
                                              static_cast<hipStream_t>(stream));

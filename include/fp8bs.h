@@ -18,7 +18,8 @@
  *     its 16-bit pattern, e4m3 as bytes (OCP E4M3FN, max 448).
  *   - stream is a hipStream_t passed as void* (NULL = the default stream).  Every
  *     call is asynchronous and stream-ordered; nothing reads device data on the
- *     host, so masked counts never leave the device.
+ *     host, so masked counts never leave the device.  Several host threads may call on
+ *     one stream: the launches of a call that uses the stream's workspace stay together.
  *   - Return value: FP8BS_OK (0) or a negative status; on error nothing is
  *     launched.  fp8bs_status_string() names a status; after FP8BS_ERR_LAUNCH,
  *     fp8bs_last_hip_error() gives the hipError_t of the failed call (per thread).

@@ -1,0 +1,207 @@
+// What the library's host code asks of the HIP runtime, call by call, without a GPU: the
+// program defines the few runtime functions that libfp8bs.so uses (its own definitions come
+// before those of the runtime), writes every launch down and starts nothing.
+// `host_launches <scenario>` prints what is wrong and returns 1, or returns 0.
+#include <hip/hip_runtime_api.h>
+
+#include <chrono>
+#include <condition_variable>
+#include <cstdio>
+#include <cstring>
+#include <functional>
+#include <map>
+#include <mutex>
+#include <string>
+#include <thread>
+#include <vector>
+
+#include "../include/fp8bs.h"
+
+namespace {
+
+struct Launch {
+  std::string kernel;  // mangled name
+  dim3 grid, block;
+  hipStream_t stream;
+  std::thread::id by;
+};
+std::mutex mu;
+std::vector<Launch> launches;
+std::function<void(const Launch&)> on_launch;  // called after a launch has been written down
+bool capturing = false;
+int allocations = 0;
+
+std::map<const void*, std::string>& kernels() {  // filled before main
+  static std::map<const void*, std::string> m;
+  return m;
+}
+struct Configuration {
+  dim3 grid, block;
+  size_t lds;
+  hipStream_t stream;
+};
+thread_local Configuration pushed;
+
+}  // namespace
+
+extern "C" {
+void** __hipRegisterFatBinary(const void*) {
+  static void* handle = nullptr;
+  return &handle;
+}
+void __hipUnregisterFatBinary(void**) {}
+void __hipRegisterFunction(void**, const void* host, char*, const char* name, unsigned, void*, void*, void*, void*,
+                           int*) {
+  kernels()[host] = name;
+}
+void __hipRegisterVar(void**, void*, char*, char*, int, size_t, int, int) {}
+hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds, hipStream_t stream) {
+  pushed = {grid, block, lds, stream};
+  return hipSuccess;
+}
+hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipStream_t* stream) {
+  *grid = pushed.grid;
+  *block = pushed.block;
+  *lds = pushed.lds;
+  *stream = pushed.stream;
+  return hipSuccess;
+}
+hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void**, size_t, hipStream_t stream) {
+  const Launch l = {kernels()[f], grid, block, stream, std::this_thread::get_id()};
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    launches.push_back(l);
+  }
+  if (on_launch) on_launch(l);
+  return hipSuccess;
+}
+hipError_t hipGetLastError() { return hipSuccess; }
+hipError_t hipGetDevice(int* dev) {
+  *dev = 0;
+  return hipSuccess;
+}
+hipError_t hipGetDevicePropertiesR0600(hipDeviceProp_tR0600* prop, int) {
+  std::memset(prop, 0, sizeof(*prop));
+  std::strcpy(prop->gcnArchName, "gfx950");
+  return hipSuccess;
+}
+hipError_t hipMalloc(void** p, size_t) {
+  static uintptr_t next = uintptr_t(1) << 40;  // never dereferenced
+  std::lock_guard<std::mutex> lk(mu);
+  ++allocations;
+  next += uintptr_t(1) << 36;
+  *p = reinterpret_cast<void*>(next);
+  return hipSuccess;
+}
+hipError_t hipFree(void*) { return hipSuccess; }
+hipError_t hipFuncSetAttribute(const void*, hipFuncAttribute, int) { return hipSuccess; }
+hipError_t hipGetSymbolAddress(void** p, const void*) { return hipMalloc(p, 0); }
+hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus* status) {
+  *status = capturing ? hipStreamCaptureStatusActive : hipStreamCaptureStatusNone;
+  return hipSuccess;
+}
+}
+
+namespace {
+
+bool failed = false;
+void expect(bool ok, const std::string& what) {
+  if (ok) return;
+  failed = true;
+  std::printf("%s\n", what.c_str());
+}
+template <typename T = void>
+T* at(uintptr_t n) {  // an aligned address that nothing reads
+  return reinterpret_cast<T*>(n << 20);
+}
+void* stream_of(uintptr_t n) { return at(1000 + n); }
+
+int norm_backward(int64_t T, int64_t N, void* stream) {
+  return residual_rms_norm_backward(at(1), N, nullptr, 0, at(2), N, 0, at(3), N, at(4), at(5), 0, at(6), 1.0f, 1e-6f,
+                                    0.0f, T, N, at(7), N, at(8), N, at<float>(9), at<float>(10), at<float>(11), 0,
+                                    stream);
+}
+int to_experts(void* stream) {
+  return fp8_quant_group_pack_to_experts(at(1), 512, 4096, 512, at<int32_t>(2), 8, 32, 64, at(3), at<uint32_t>(4),
+                                         at<int32_t>(5), at<int32_t>(6), stream);
+}
+int split_gemm(void* stream) {
+  return fp8_block_gemm_nt(at(1), at<uint32_t>(2), 64, at(3), at<float>(4), at(5), 7168, 64, 7168, 18432, stream);
+}
+
+// A call whose launches share the stream's workspace is not broken into by another host
+// thread's call on that stream, which would overwrite what the first one's later launches
+// read; calls on other streams do not wait for it.
+void threads() {
+  struct Call {
+    const char* name;
+    std::function<int(void*)> run;
+    size_t launches;
+  };
+  Call calls[] = {{"norm backward", [](void* s) { return norm_backward(512, 2048, s); }, 0},
+                  {"quantization into the experts' layout", to_experts, 0},
+                  {"split GEMM", split_gemm, 0}};
+  for (int round = 0; round < 2; ++round)  // the first round allocates, which clears the counters with a launch
+    for (Call& c : calls)
+      for (int s = 0; s < 2; ++s) {
+        launches.clear();
+        expect(c.run(stream_of(s)) == FP8BS_OK, std::string(c.name) + " failed");
+        c.launches = launches.size();
+      }
+  for (const Call& first : calls) {
+    expect(first.launches == 2, std::string(first.name) + ": not two launches");
+    for (const Call& second : calls) {
+      for (int other = 0; other < 2; ++other) {
+        launches.clear();
+        std::mutex m;
+        std::condition_variable cv;
+        bool started = false, answered = false;
+        std::thread::id a_id;
+        on_launch = [&](const Launch& l) {
+          std::unique_lock<std::mutex> lk(m);
+          if (l.by == a_id && !started) {  // the first launch: give the other thread time for its call
+            started = true;
+            cv.notify_all();
+            cv.wait_for(lk, std::chrono::milliseconds(other ? 5000 : 100), [&] { return answered; });
+          } else if (l.by != a_id) {
+            answered = true;
+            cv.notify_all();
+          }
+        };
+        std::thread a([&] {
+          {
+            std::lock_guard<std::mutex> lk(m);
+            a_id = std::this_thread::get_id();
+          }
+          expect(first.run(stream_of(0)) == FP8BS_OK, std::string(first.name) + " failed");
+        });
+        std::thread b([&] {
+          std::unique_lock<std::mutex> lk(m);
+          cv.wait(lk, [&] { return started; });
+          lk.unlock();
+          expect(second.run(stream_of(other)) == FP8BS_OK, std::string(second.name) + " failed");
+        });
+        const std::thread::id b_id = b.get_id();
+        a.join();
+        b.join();
+        on_launch = nullptr;
+        std::string order;
+        for (const Launch& l : launches) order += l.by == b_id ? 'b' : 'a';
+        const std::string as(first.launches, 'a'), bs(second.launches, 'b');
+        if (other)
+          expect(order[1] == 'b', std::string(second.name) + " on another stream waits for " + first.name + ": " + order);
+        else
+          expect(order == as + bs, std::string(second.name) + " breaks into " + first.name + ": " + order);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int main(int argc, char** argv) {
+  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}};
+  if (argc != 2 || scenarios.count(argv[1]) == 0) return 2;
+  scenarios.at(argv[1])();
+  return failed ? 1 : 0;
+}

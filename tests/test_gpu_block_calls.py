@@ -1,0 +1,82 @@
+"""Ways of calling the operators around the experts' products: from several host threads,
+under graph capture, and at the ends of their sizes."""
+import threading
+
+import pytest
+import torch
+
+import block_scaled_fp8_token_amd as F
+from block_scaled_fp8_token_amd import _lib
+from gpu_helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def norm_backward_into(a, d_w, stream):
+    """The C entry: gradients of a norm with a branch, its weight gradients into d_w [3, N]."""
+    T, N = a["h"].shape
+    p = {n: t.data_ptr() for n, t in a.items()}
+    return _lib.residual_rms_norm_backward(
+        p["dz"], N, p["dh"], N, p["h"], N, 0, p["y"], N, p["w"], p["w"], 0, p["w"], 1.0, 1e-6, 0.0, T, N, p["dx"], N,
+        p["dy"], N, d_w[0].data_ptr(), d_w[1].data_ptr(), d_w[2].data_ptr(), 0, stream)
+
+
+def norm_state(seed, T, N):
+    torch.manual_seed(seed)
+    a = {n: torch.randn(T, N, device=DEV).to(BF) for n in ("dz", "dh", "h", "y")}
+    a.update(w=torch.randn(N, device=DEV).to(BF), dx=torch.empty(T, N, dtype=BF, device=DEV),
+             dy=torch.empty(T, N, dtype=BF, device=DEV))
+    return a
+
+
+def test_host_threads_on_one_stream():
+    # calls whose launches share the stream's workspace: norm backward, dispatch, a split GEMM
+    calls, T, N, E, M, K = 60, 300, 1024, 16, 64, 512
+    states = [norm_state(s, T, N) for s in (1, 2)]
+    x = torch.randn(512, K, device=DEV).to(BF)
+    ids = torch.randint(0, E, (512, 4), device=DEV, dtype=torch.int32)
+    qa, sfa = F.fp8_quant_group_pack(torch.randn(64, 4096, device=DEV).to(BF))
+    qb, sfb = F.fp8_block_quant_128x128(torch.randn(1024, 4096, device=DEV).to(BF))
+    assert F.gemm_config(F.LAYOUT_DENSE, 64, 1024, 4096)["splits"] > 1
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    grads = [torch.empty(calls, 3, N, device=DEV) for _ in states]
+    slots = torch.full((calls, 512, 4), -7, dtype=torch.int32, device=DEV)
+    counts = torch.empty(calls, E, dtype=torch.int32, device=DEV)
+    q = torch.empty(E, M, K, dtype=torch.uint8, device=DEV)
+    sf = torch.empty(E, 1, M, dtype=torch.int32, device=DEV)
+    c = torch.empty(calls, 64, 1024, dtype=BF, device=DEV)
+    errors = []
+
+    def norm(i, n):
+        st = norm_backward_into(states[i], grads[i][n], stream.cuda_stream)
+        if st:
+            errors.append(st)
+
+    def dispatch(n):
+        F.fp8_quant_group_pack_to_experts(x, ids, E, M, q=q, sf=sf, masked_m=counts[n], slot_of=slots[n], stream=stream)
+
+    def gemm(n):
+        F.fp8_block_gemm_nt(qa, sfa, qb, sfb, c=c[n], stream=stream)
+
+    work = [lambda n: norm(0, n), lambda n: norm(1, n), dispatch, gemm]
+    for fn in work:  # alone: call 0 of each, also the workspace's size
+        fn(0)
+    stream.synchronize()
+    together = threading.Barrier(len(work))
+
+    def many(fn):
+        together.wait()
+        for n in range(1, calls):
+            fn(n)
+    threads = [threading.Thread(target=many, args=(fn,)) for fn in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    stream.synchronize()
+    assert not errors
+    for got in (*grads, slots, counts, c):
+        assert (got == got[:1]).all()
