@@ -160,9 +160,19 @@ unsigned threads_of(int64_t N, int64_t parts) { return (unsigned)((N / 8 + 64 * 
 hipError_t launch_combine(const CombineProblem& p, const uint16_t* y, const uint16_t* base, int64_t ld_base,
                           uint16_t* out, int64_t ld_out, hipStream_t stream) {
   const unsigned tiles = (unsigned)((p.N / 8 + 255) / 256);
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)(p.T * tiles)), dim3(threads_of(p.N, tiles)), 0, stream, p.ids,
-                     p.slots, p.weights, p.topk, p.E, p.M_max, p.N, y, base, ld_base, out, ld_out, tiles);
-  return hipGetLastError();
+  // 2^24 workgroups of 256 are 2^32 threads, one more than a launch takes: tokens past 2^23
+  // workgroups go to launches of their own
+  const int64_t most = (1 << 23) / tiles;
+  for (int64_t t0 = 0; t0 < p.T; t0 += most) {
+    const int64_t T = p.T - t0 < most ? p.T - t0 : most, pair = t0 * p.topk;
+    hipLaunchKernelGGL(combine_kernel, dim3((unsigned)(T * tiles)), dim3(threads_of(p.N, tiles)), 0, stream,
+                       p.ids + pair, p.slots + pair, p.weights != nullptr ? p.weights + pair : nullptr, p.topk, p.E,
+                       p.M_max, p.N, y, base != nullptr ? base + t0 * ld_base : nullptr, ld_base, out + t0 * ld_out,
+                       ld_out, tiles);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_combine_backward(const CombineProblem& p, const uint16_t* d_out, int64_t ld_d, const uint16_t* y,

@@ -265,7 +265,8 @@ bool aligned_or_null(const void* p, uintptr_t a) { return p == nullptr || aligne
 bool bad_rows(const void* p, int64_t ld, int64_t N) { return p != nullptr && ld < N; }
 bool misaligned_rows(const void* p, int64_t ld) { return p != nullptr && (!aligned(p, 16) || ld % 8 != 0); }
 
-// Tokens of one call: what keeps every grid under 2^32 threads.
+// Tokens of one call: with it every grid is under 2^32 threads (the combine's, which has a
+// workgroup for each 2048 columns of a token, as launches of at most 2^23 workgroups).
 constexpr int64_t kMostRows = 1 << 22;
 
 int check_route(int64_t ld, int64_t T, int64_t E, int32_t logits_f32, int32_t scoring, int32_t topk) {

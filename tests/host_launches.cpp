@@ -24,6 +24,7 @@ struct Launch {
   dim3 grid, block;
   hipStream_t stream;
   std::thread::id by;
+  void** args;  // only inside on_launch
 };
 std::mutex mu;
 std::vector<Launch> launches;
@@ -66,8 +67,8 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
   *stream = pushed.stream;
   return hipSuccess;
 }
-hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void**, size_t, hipStream_t stream) {
-  const Launch l = {kernels()[f], grid, block, stream, std::this_thread::get_id()};
+hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, size_t, hipStream_t stream) {
+  const Launch l = {kernels()[f], grid, block, stream, std::this_thread::get_id(), args};
   {
     std::lock_guard<std::mutex> lk(mu);
     launches.push_back(l);
@@ -197,10 +198,61 @@ void threads() {
   }
 }
 
+// The largest sizes of the operators around the experts' products: no launch may have 2^32
+// threads in one dimension, and a combine that takes several covers every token once.
+void limits() {
+  const int64_t T = int64_t(1) << 22;
+  struct Size {
+    int64_t T, N;
+  };
+  for (const Size s : {Size{T, 8192}, Size{T, 7168}, Size{T, 6152}, Size{1 << 15, 1 << 20}, Size{(1 << 15) - 1, 1 << 20},
+                       Size{5, 8192}}) {
+    const int64_t ld = s.N + 8, topk = 3;
+    int64_t tokens = 0;
+    launches.clear();
+    on_launch = [&](const Launch& l) {
+      auto arg = [&](int i) { return *static_cast<uintptr_t*>(l.args[i]); };
+      // ids, slots, weights, .., base (8), its stride, out (10), its stride, tiles
+      for (int i : {0, 1, 2})
+        expect(arg(i) - reinterpret_cast<uintptr_t>(at(2 + i)) == uintptr_t(tokens * topk * 4), "pairs of another token");
+      for (int i : {8, 10})
+        expect(arg(i) - reinterpret_cast<uintptr_t>(at(i)) == uintptr_t(tokens * ld * 2), "rows of another token");
+      const unsigned tiles = *static_cast<unsigned*>(l.args[12]);
+      expect(int64_t(tiles) * l.block.x * 8 >= s.N, "columns left out");
+      expect(l.grid.x % tiles == 0, "part of a token");
+      tokens += l.grid.x / tiles;
+    };
+    expect(moe_combine(at(1), at<int32_t>(2), at<int32_t>(3), at<float>(4), at(8), ld, s.T, topk, 4, 8, s.N, at(10), ld,
+                       stream_of(0)) == FP8BS_OK, "combine refused");
+    on_launch = nullptr;
+    expect(tokens == s.T, "combine of " + std::to_string(tokens) + " tokens for " + std::to_string(s.T));
+    expect(s.T > 5 || launches.size() == 1, "more launches than one for a small combine");
+    for (const Launch& l : launches)
+      expect(uint64_t(l.grid.x) * l.block.x < (uint64_t(1) << 32),
+             "combine " + std::to_string(s.T) + " x " + std::to_string(s.N) + ": 2^32 threads");
+  }
+  expect(moe_combine(at(1), at<int32_t>(2), at<int32_t>(3), nullptr, nullptr, 0, T, 1, 4, 8, 8200, at(5), 8200, nullptr) ==
+             FP8BS_ERR_SHAPE, "combine past the stated limit");
+  launches.clear();
+  expect(moe_route_topk(at(1), 1, 1024, T, 1024, nullptr, FP8BS_SIGMOID, 1, 1, 1, 64, 1, 1.0f, at<int32_t>(2),
+                        at<float>(3), nullptr) == FP8BS_OK, "route refused");
+  expect(moe_route_topk(at(1), 0, 256, T, 256, nullptr, FP8BS_SOFTMAX, 1, 1, 1, 8, 1, 1.0f, at<int32_t>(2), at<float>(3),
+                        nullptr) == FP8BS_OK, "route refused");
+  expect(moe_route_topk_backward(at(1), 1, 1024, T, 1024, at<int32_t>(2), at<float>(3), FP8BS_SOFTMAX, 64, 0, 1.0f,
+                                 at(4), 1024, nullptr) == FP8BS_OK, "route backward refused");
+  expect(moe_combine_backward(at(1), 8192, at(2), at<int32_t>(3), at<int32_t>(4), at<float>(5), T, 64, 4, 8, 8192, at(6),
+                              nullptr, nullptr, at<float>(7), nullptr) == FP8BS_OK, "combine backward refused");
+  expect(norm_backward(T, 16384, nullptr) == FP8BS_OK, "norm backward refused");
+  expect(residual_rms_norm(at(1), 16384, 1, nullptr, 0, nullptr, nullptr, 0, at(2), 1.0f, 1e-6f, 0.0f, T, 16384, at(3),
+                           16384, nullptr, 0, nullptr, 0, nullptr, 0, nullptr) == FP8BS_OK, "norm refused");
+  for (const Launch& l : launches)
+    expect(uint64_t(l.grid.x) * l.block.x < (uint64_t(1) << 32) && l.grid.y <= 65535, l.kernel + ": grid too large");
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}};
+  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}, {"limits", limits}};
   if (argc != 2 || scenarios.count(argv[1]) == 0) return 2;
   scenarios.at(argv[1])();
   return failed ? 1 : 0;

@@ -80,3 +80,18 @@ def test_host_threads_on_one_stream():
     assert not errors
     for got in (*grads, slots, counts, c):
         assert (got == got[:1]).all()
+
+
+def test_combine_of_more_tokens_than_a_launch_takes():
+    # three workgroups a token: the tokens past 2^23 workgroups are a second launch (34 GB of output)
+    T, N, E, M = 1 << 22, 4104, 2, 4
+    y = torch.randn(E, M, N, device=DEV).to(BF)
+    pair = torch.randint(0, E * M, (T, 1), device=DEV, dtype=torch.int32)
+    w = torch.randint(1, 5, (T, 1), device=DEV).float()
+    out = F.moe_combine(y, pair // M, pair % M, w)
+    for t in range(0, T, 1 << 18):
+        rows = slice(t, t + (1 << 18))
+        want = (y.view(E * M, N).float()[pair[rows, 0].long()] * w[rows]).to(BF)
+        assert torch.equal(out[rows], want), "tokens from %d" % t
+    del out, want
+    torch.cuda.empty_cache()

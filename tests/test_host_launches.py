@@ -31,3 +31,7 @@ def run(program, scenario):
 
 def test_threads_on_one_stream(program):
     run(program, "threads")
+
+
+def test_largest_sizes(program):
+    run(program, "limits")
