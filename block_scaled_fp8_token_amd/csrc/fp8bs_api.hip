@@ -721,7 +721,16 @@ int moe_combine_backward(const void* d_out, int64_t ld_d, const void* y, const i
                          const int32_t* slot_of, const float* weights, int64_t T, int32_t topk, int64_t E,
                          int64_t M_max, int64_t N, void* d_y, void* q, uint32_t* sf, float* d_weights, void* stream) {
   int st = check_combine(T, topk, E, M_max, N);
-  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (st < 0) return st;
+  if (st > 0) {
+    if (T == 0 || d_weights == nullptr) return FP8BS_OK;
+    // no columns: the weights' gradients are sums of nothing
+    if (!aligned(d_weights, 4)) return FP8BS_ERR_ALIGN;
+    st = check_device();
+    if (st != FP8BS_OK) return st;
+    hipError_t e = zero_words(d_weights, (size_t)T * topk * sizeof(float), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+  }
   const bool rows = E > 0 && M_max > 0;  // a layout without rows has no pointers
   if (!d_out || !topk_ids || !slot_of || (rows && (!d_y == !q || !q != !sf || (d_weights && !y)))) return FP8BS_ERR_NULL;
   if (ld_d < N || (q && N % 128 != 0)) return FP8BS_ERR_SHAPE;

@@ -387,7 +387,7 @@ int moe_route_topk_backward(const void* logits, int32_t logits_f32, int64_t ld, 
  * (d_y [E][M_max][N]) or, with d_y = NULL, as q e4m3 [E][M_max][N] and sf uint32
  * [E][ceil(N/512)][M_max] quantized as fp8_quant_group_pack quantizes the fp32 values
  * (N % 128 == 0), ready for the masked GEMM that takes the gradient on; and d_weights[t][j] =
- * <d_out[t], y[e][s]> (0 for a pair without a row; NULL: not wanted, and y is not read).
+ * <d_out[t], y[e][s]> (0 for a pair without a row, or with N == 0; NULL: not wanted, and y is not read).
  * No two pairs may name the same row.
  */
 int moe_combine(const void* y, const int32_t* topk_ids, const int32_t* slot_of, const float* weights, const void* base,

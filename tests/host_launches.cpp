@@ -249,10 +249,32 @@ void limits() {
     expect(uint64_t(l.grid.x) * l.block.x < (uint64_t(1) << 32) && l.grid.y <= 65535, l.kernel + ": grid too large");
 }
 
+// A dot product over no columns is zero, and is written.
+void no_columns() {
+  launches.clear();
+  uintptr_t cleared = 0;
+  int64_t words = 0;
+  on_launch = [&](const Launch& l) {
+    expect(l.kernel.find("zero_words") != std::string::npos, l.kernel + " over no columns");
+    cleared = *static_cast<uintptr_t*>(l.args[0]);
+    words = *static_cast<int64_t*>(l.args[1]);
+  };
+  expect(moe_combine_backward(nullptr, 0, nullptr, at<int32_t>(3), at<int32_t>(4), at<float>(5), 7, 3, 4, 8, 0, nullptr,
+                              nullptr, nullptr, at<float>(7), nullptr) == FP8BS_OK, "combine backward refused");
+  on_launch = nullptr;
+  expect(cleared == reinterpret_cast<uintptr_t>(at(7)) && words == 21, "weights' gradients of no columns not cleared");
+  launches.clear();
+  expect(moe_combine_backward(nullptr, 0, nullptr, nullptr, nullptr, nullptr, 7, 3, 4, 8, 0, nullptr, nullptr, nullptr,
+                              nullptr, nullptr) == FP8BS_OK, "combine backward without weights refused");
+  expect(moe_combine_backward(nullptr, 0, nullptr, nullptr, nullptr, nullptr, 0, 3, 4, 8, 0, nullptr, nullptr, nullptr,
+                              at<float>(7), nullptr) == FP8BS_OK, "combine backward of nothing refused");
+  expect(launches.empty(), "a launch without anything to write");
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}, {"limits", limits}};
+  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}, {"limits", limits}, {"no_columns", no_columns}};
   if (argc != 2 || scenarios.count(argv[1]) == 0) return 2;
   scenarios.at(argv[1])();
   return failed ? 1 : 0;

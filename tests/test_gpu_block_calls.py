@@ -95,3 +95,14 @@ def test_combine_of_more_tokens_than_a_launch_takes():
         assert torch.equal(out[rows], want), "tokens from %d" % t
     del out, want
     torch.cuda.empty_cache()
+
+
+def test_combine_backward_of_no_columns():
+    ids = torch.zeros(3, 2, dtype=torch.int32, device=DEV)
+    w = torch.ones(3, 2, device=DEV)
+    y, d_out = torch.empty(2, 4, 0, dtype=BF, device=DEV), torch.empty(3, 0, dtype=BF, device=DEV)
+    d_w = torch.full((3, 2), float("nan"), device=DEV)
+    d_y, got = F.moe_combine_backward(d_out, y, ids, ids, w, d_weights=d_w)
+    assert got is d_w and torch.equal(d_w, torch.zeros_like(d_w)) and d_y.shape == (2, 4, 0)
+    _, got = F.moe_combine_backward(d_out, y, ids, ids)
+    assert got is None

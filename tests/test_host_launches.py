@@ -35,3 +35,7 @@ def test_threads_on_one_stream(program):
 
 def test_largest_sizes(program):
     run(program, "limits")
+
+
+def test_combine_backward_without_columns(program):
+    run(program, "no_columns")
