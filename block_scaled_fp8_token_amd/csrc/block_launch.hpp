@@ -68,7 +68,7 @@ struct NormGradients {
   void* d_gate;  // fp32 [N] if ld_gate == 0, else bf16 [T][ld_dgate]
   int64_t ld_dgate;
 };
-// partials: norm_backward_scratch_bytes() of device memory.
+// partials: norm_backward_scratch_bytes() of device memory (none: not read).
 hipError_t launch_norm_backward(const NormProblem& p, const NormGradients& g, float* partials, hipStream_t stream);
 size_t norm_backward_scratch_bytes(const NormProblem& p);
 

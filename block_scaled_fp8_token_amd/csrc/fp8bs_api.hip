@@ -809,14 +809,15 @@ int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, 
                                             weight_offset, T, N);
   const fp8bs::NormGradients g = {static_cast<const uint16_t*>(d_z), ld_dz, d_h, ld_dh, h, ldh, d_x, ld_dx,
                                   static_cast<uint16_t*>(d_y), ld_dy, d_w_pre, d_w_post, d_gate, ld_dgate};
-  // partial sums live in the stream's workspace past the split-K arrival counters
-  const size_t off = fp8bs::gemm_workspace_zeroed_prefix();
+  // partial sums live in the stream's workspace past the split-K arrival counters; one workgroup
+  // has none
+  const size_t off = fp8bs::gemm_workspace_zeroed_prefix(), sums = fp8bs::norm_backward_scratch_bytes(p);
   void* ws = nullptr;
   std::unique_lock<std::mutex> held;
-  st = get_workspace(off + fp8bs::norm_backward_scratch_bytes(p), static_cast<hipStream_t>(stream), &ws, &held);
+  st = get_workspace(sums > 0 ? off + sums : 0, static_cast<hipStream_t>(stream), &ws, &held);
   if (st != FP8BS_OK) return st;
-  hipError_t e = fp8bs::launch_norm_backward(p, g, reinterpret_cast<float*>(static_cast<char*>(ws) + off),
-                                             static_cast<hipStream_t>(stream));
+  float* const partials = sums > 0 ? reinterpret_cast<float*>(static_cast<char*>(ws) + off) : nullptr;
+  hipError_t e = fp8bs::launch_norm_backward(p, g, partials, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FP8BS_OK : fail_hip(e);
 }
 

@@ -271,10 +271,22 @@ void no_columns() {
   expect(launches.empty(), "a launch without anything to write");
 }
 
+// One row has no partial sums: its norm backward allocates nothing, also under capture.
+void one_row() {
+  allocations = 0;
+  capturing = true;
+  launches.clear();
+  for (int64_t N : {int64_t(8), int64_t(7168), int64_t(16384)})
+    expect(norm_backward(1, N, stream_of(0)) == FP8BS_OK, "norm backward of one row refused under capture");
+  expect(launches.size() == 3 && allocations == 0, "norm backward of one row: not one launch and no allocation");
+  expect(norm_backward(2, 8, stream_of(0)) == FP8BS_ERR_ALLOC, "an allocation under capture");
+  capturing = false;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}, {"limits", limits}, {"no_columns", no_columns}};
+  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}, {"limits", limits}, {"no_columns", no_columns}, {"one_row", one_row}};
   if (argc != 2 || scenarios.count(argv[1]) == 0) return 2;
   scenarios.at(argv[1])();
   return failed ? 1 : 0;

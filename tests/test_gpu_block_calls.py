@@ -1,5 +1,6 @@
 """Ways of calling the operators around the experts' products: from several host threads,
 under graph capture, and at the ends of their sizes."""
+import ctypes
 import threading
 
 import pytest
@@ -29,6 +30,14 @@ def norm_state(seed, T, N):
     a.update(w=torch.randn(N, device=DEV).to(BF), dx=torch.empty(T, N, dtype=BF, device=DEV),
              dy=torch.empty(T, N, dtype=BF, device=DEV))
     return a
+
+
+def unused_stream():
+    """A stream that no call of the library has seen (torch's own come from a pool and come again)."""
+    path = next(line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line)
+    handle = ctypes.c_void_p()
+    assert ctypes.CDLL(path).hipStreamCreateWithFlags(ctypes.byref(handle), 1) == 0  # not blocking
+    return torch.cuda.ExternalStream(handle.value)
 
 
 def test_host_threads_on_one_stream():
@@ -106,3 +115,24 @@ def test_combine_backward_of_no_columns():
     assert got is d_w and torch.equal(d_w, torch.zeros_like(d_w)) and d_y.shape == (2, 4, 0)
     _, got = F.moe_combine_backward(d_out, y, ids, ids)
     assert got is None
+
+
+def test_norm_backward_of_one_row_captured_first():
+    N = 1024
+    a = norm_state(3, 1, N)
+    want, got = torch.empty(3, N, device=DEV), torch.empty(3, N, device=DEV)
+    assert norm_backward_into(a, want, torch.cuda.current_stream().cuda_stream) == 0
+    rows = a["dx"].clone(), a["dy"].clone()
+    torch.cuda.synchronize()
+    stream, graph = unused_stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        status = norm_backward_into(a, got, stream.cuda_stream)
+    assert status == 0
+    for _ in range(4):
+        for t in (got, a["dx"], a["dy"]):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(a["dx"], rows[0]) and torch.equal(a["dy"], rows[1])
+        norm_backward_into(norm_state(4, 1, N), torch.empty(3, N, device=DEV), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()

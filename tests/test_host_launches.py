@@ -39,3 +39,7 @@ def test_largest_sizes(program):
 
 def test_combine_backward_without_columns(program):
     run(program, "no_columns")
+
+
+def test_norm_backward_of_one_row_allocates_nothing(program):
+    run(program, "one_row")
