@@ -80,6 +80,9 @@ _SIGS = {
                           _P, _I64, _P, _I64, _P],
     "residual_rms_norm_backward": [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _F32, _F32, _F32,
                                    _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P],
+    "residual_rms_norm_backward_scratch_bytes": [_I64, _I64],
+    "residual_rms_norm_backward_noalloc": [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _F32, _F32,
+                                           _F32, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P],
     "silu_mul_quant_group_pack_checkpoint": [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P],
     "silu_mul_backward_from_checkpoint": [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P],
     "fp8bs_gemm_config_count": [],
@@ -95,7 +98,8 @@ for _name, _args in _SIGS.items():
         raise ImportError("libfp8bs.so does not export %s: it is older than the sources; rebuild with "
                           "`python block_scaled_fp8_token_amd/build.py`" % _name) from None
     _fn.argtypes = _args
-    _fn.restype = ctypes.c_char_p if _name == "fp8bs_status_string" else ctypes.c_int
+    _fn.restype = {"fp8bs_status_string": ctypes.c_char_p,
+                   "residual_rms_norm_backward_scratch_bytes": _I64}.get(_name, ctypes.c_int)
 
 
 class Fp8bsError(RuntimeError):

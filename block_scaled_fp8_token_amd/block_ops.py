@@ -298,7 +298,8 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
                                d_gate: torch.Tensor | None = None, stream=None):
     """Gradients of residual_rms_norm: from d_z bf16 [T, N], the h it returned and (with the residual stream's
     gradient d_h, of h's type) -> (d_x, d_y, d_w_pre, d_w_post, d_gate), None for parts that are not there.  d_x has h's
-    type, d_y is bf16, the weights' gradients are fp32 [N]; d_gate is fp32 [N] for a gate [N] and bf16 [T, N] else."""
+    type, d_y is bf16, the weights' gradients are fp32 [N]; d_gate is fp32 [N] for a gate [N] and bf16 [T, N] else.
+    Equal calls give equal bits.  The call's partial sums (at most 52 MB) come from torch's allocator."""
     if stream is not None:
         return _on_stream(stream, residual_rms_norm_backward, d_z, h, w_pre, d_h, y, w_post, gate, residual_scale,
                           eps, weight_offset, d_x, d_y, d_w_pre, d_w_post, d_gate)
@@ -326,10 +327,13 @@ def residual_rms_norm_backward(d_z: torch.Tensor, h: torch.Tensor, w_pre: torch.
             d_gate, pdg = _out(d_gate, "d_gate", _F32, (N,), h)
         else:
             d_gate, pdg, ld_dg = _out_rows(d_gate, "d_gate", _BF16, T, N, h)
-    _launch("residual_rms_norm_backward",
+    # partial sums from torch's allocator (the stream's, or a capture's own memory), not the library's workspace
+    need = _lib.residual_rms_norm_backward_scratch_bytes(T, N)
+    scratch = h.new_empty(need // 4, dtype=torch.float32) if need else None
+    _launch("residual_rms_norm_backward_noalloc",
             (d_z, d_h, h, y, w_post, gate, w_pre), pz, ld_z, pdh, ld_dh, ph, ldh,
             h.dtype == torch.float32, py, ldy, pwp, pg, ld_g, pw, residual_scale, eps, weight_offset, T, N, pdx, ld_dx,
-            pdy, ld_dy, pdw, pdwp, pdg, ld_dg)
+            pdy, ld_dy, pdw, pdwp, pdg, ld_dg, None if scratch is None else scratch.data_ptr(), need)
     return d_x, d_y, d_w_pre, d_w_post, d_gate
 
 

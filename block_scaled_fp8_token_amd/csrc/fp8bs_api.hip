@@ -333,6 +333,62 @@ fp8bs::NormProblem norm_problem(int32_t residual_f32, const void* y, int64_t ldy
   return p;
 }
 
+// The norm's backward pass with its partial sums in `scratch` (given), or else in the stream's
+// workspace.
+int run_norm_backward(bool given, void* scratch, int64_t scratch_bytes, const void* d_z, int64_t ld_dz, const void* d_h,
+                      int64_t ld_dh, const void* h, int64_t ldh, int32_t residual_f32, const void* y, int64_t ldy,
+                      const void* w_post, const void* gate, int64_t ld_gate, const void* w_pre, float residual_scale,
+                      float eps, float weight_offset, int64_t T, int64_t N, void* d_x, int64_t ld_dx, void* d_y,
+                      int64_t ld_dy, float* d_w_pre, float* d_w_post, void* d_gate, int64_t ld_dgate, void* stream) {
+  if (T < 0 || N < 0 || N % 8 != 0 || N > fp8bs::kNormMaxN) return FP8BS_ERR_SHAPE;
+  if (T == 0) {
+    if (N == 0) return FP8BS_OK;
+    if (!d_w_pre) return FP8BS_ERR_NULL;
+    int st = check_device();
+    if (st != FP8BS_OK) return st;
+    float* sums[3] = {d_w_pre, d_w_post, ld_gate == 0 ? static_cast<float*>(d_gate) : nullptr};
+    for (float* s : sums) {
+      if (s == nullptr) continue;
+      if (!aligned(s, 16)) return FP8BS_ERR_ALIGN;
+      hipError_t e = zero_words(s, (size_t)N * sizeof(float), static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return fail_hip(e);
+    }
+    return FP8BS_OK;
+  }
+  int st = check_norm(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, T, N);
+  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
+  if (!d_z || !h || !d_x || !d_w_pre || !y != !d_y || !w_post != !d_w_post || !gate != !d_gate) return FP8BS_ERR_NULL;
+  if (ld_dz < N || bad_rows(d_h, ld_dh, N) || ldh < N || ld_dx < N || bad_rows(d_y, ld_dy, N) ||
+      (gate && ld_gate != 0 && ld_dgate < N))
+    return FP8BS_ERR_SHAPE;
+  if (misaligned_rows(d_z, ld_dz) || misaligned_rows(d_h, ld_dh) || misaligned_rows(h, ldh) ||
+      misaligned_rows(d_x, ld_dx) || misaligned_rows(d_y, ld_dy) || !aligned(d_w_pre, 16) ||
+      !aligned_or_null(d_w_post, 16) || !aligned_or_null(d_gate, 16) || (gate && ld_gate != 0 && ld_dgate % 8 != 0))
+    return FP8BS_ERR_ALIGN;
+  const fp8bs::NormProblem p = norm_problem(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, residual_scale, eps,
+                                            weight_offset, T, N);
+  const size_t sums = fp8bs::norm_backward_scratch_bytes(p);
+  if (given && sums > 0) {
+    if (!scratch) return FP8BS_ERR_NULL;
+    if (!aligned(scratch, 16)) return FP8BS_ERR_ALIGN;
+    if (scratch_bytes < (int64_t)sums) return FP8BS_ERR_SCRATCH;
+  }
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::NormGradients g = {static_cast<const uint16_t*>(d_z), ld_dz, d_h, ld_dh, h, ldh, d_x, ld_dx,
+                                  static_cast<uint16_t*>(d_y), ld_dy, d_w_pre, d_w_post, d_gate, ld_dgate};
+  std::unique_lock<std::mutex> held;
+  if (!given && sums > 0) {  // past the split-K arrival counters
+    const size_t off = fp8bs::gemm_workspace_zeroed_prefix();
+    void* ws = nullptr;
+    st = get_workspace(off + sums, static_cast<hipStream_t>(stream), &ws, &held);
+    if (st != FP8BS_OK) return st;
+    scratch = static_cast<char*>(ws) + off;
+  }
+  hipError_t e = fp8bs::launch_norm_backward(p, g, static_cast<float*>(scratch), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
 int check_checkpoint(int64_t E, int64_t M_max, int64_t H) {
   if (E < 0 || E > fp8bs::kCheckpointMaxE || M_max < 0 || H < 0 || H % 128 != 0) return FP8BS_ERR_SHAPE;
   if (M_max > INT32_MAX || E * M_max > INT32_MAX || H > (1 << 28)) return FP8BS_ERR_SHAPE;
@@ -778,47 +834,29 @@ int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, 
                                float weight_offset, int64_t T, int64_t N, void* d_x, int64_t ld_dx, void* d_y,
                                int64_t ld_dy, float* d_w_pre, float* d_w_post, void* d_gate, int64_t ld_dgate,
                                void* stream) {
-  if (T < 0 || N < 0 || N % 8 != 0 || N > fp8bs::kNormMaxN) return FP8BS_ERR_SHAPE;
-  if (T == 0) {
-    if (N == 0) return FP8BS_OK;
-    if (!d_w_pre) return FP8BS_ERR_NULL;
-    int st = check_device();
-    if (st != FP8BS_OK) return st;
-    float* sums[3] = {d_w_pre, d_w_post, ld_gate == 0 ? static_cast<float*>(d_gate) : nullptr};
-    for (float* s : sums) {
-      if (s == nullptr) continue;
-      if (!aligned(s, 16)) return FP8BS_ERR_ALIGN;
-      hipError_t e = zero_words(s, (size_t)N * sizeof(float), static_cast<hipStream_t>(stream));
-      if (e != hipSuccess) return fail_hip(e);
-    }
-    return FP8BS_OK;
-  }
-  int st = check_norm(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, T, N);
-  if (st != FP8BS_OK) return st > 0 ? FP8BS_OK : st;
-  if (!d_z || !h || !d_x || !d_w_pre || !y != !d_y || !w_post != !d_w_post || !gate != !d_gate) return FP8BS_ERR_NULL;
-  if (ld_dz < N || bad_rows(d_h, ld_dh, N) || ldh < N || ld_dx < N || bad_rows(d_y, ld_dy, N) ||
-      (gate && ld_gate != 0 && ld_dgate < N))
-    return FP8BS_ERR_SHAPE;
-  if (misaligned_rows(d_z, ld_dz) || misaligned_rows(d_h, ld_dh) || misaligned_rows(h, ldh) ||
-      misaligned_rows(d_x, ld_dx) || misaligned_rows(d_y, ld_dy) || !aligned(d_w_pre, 16) ||
-      !aligned_or_null(d_w_post, 16) || !aligned_or_null(d_gate, 16) || (gate && ld_gate != 0 && ld_dgate % 8 != 0))
-    return FP8BS_ERR_ALIGN;
-  st = check_device();
-  if (st != FP8BS_OK) return st;
-  const fp8bs::NormProblem p = norm_problem(residual_f32, y, ldy, w_post, gate, ld_gate, w_pre, residual_scale, eps,
-                                            weight_offset, T, N);
-  const fp8bs::NormGradients g = {static_cast<const uint16_t*>(d_z), ld_dz, d_h, ld_dh, h, ldh, d_x, ld_dx,
-                                  static_cast<uint16_t*>(d_y), ld_dy, d_w_pre, d_w_post, d_gate, ld_dgate};
-  // partial sums live in the stream's workspace past the split-K arrival counters; one workgroup
-  // has none
-  const size_t off = fp8bs::gemm_workspace_zeroed_prefix(), sums = fp8bs::norm_backward_scratch_bytes(p);
-  void* ws = nullptr;
-  std::unique_lock<std::mutex> held;
-  st = get_workspace(sums > 0 ? off + sums : 0, static_cast<hipStream_t>(stream), &ws, &held);
-  if (st != FP8BS_OK) return st;
-  float* const partials = sums > 0 ? reinterpret_cast<float*>(static_cast<char*>(ws) + off) : nullptr;
-  hipError_t e = fp8bs::launch_norm_backward(p, g, partials, static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+  return run_norm_backward(false, nullptr, 0, d_z, ld_dz, d_h, ld_dh, h, ldh, residual_f32, y, ldy, w_post, gate,
+                           ld_gate, w_pre, residual_scale, eps, weight_offset, T, N, d_x, ld_dx, d_y, ld_dy, d_w_pre,
+                           d_w_post, d_gate, ld_dgate, stream);
+}
+
+int64_t residual_rms_norm_backward_scratch_bytes(int64_t T, int64_t N) {
+  if (T <= 0 || N <= 0 || N % 8 != 0 || N > fp8bs::kNormMaxN) return 0;
+  fp8bs::NormProblem p = {};
+  p.T = T;
+  p.N = N;
+  return (int64_t)fp8bs::norm_backward_scratch_bytes(p);
+}
+
+int residual_rms_norm_backward_noalloc(const void* d_z, int64_t ld_dz, const void* d_h, int64_t ld_dh, const void* h,
+                                       int64_t ldh, int32_t residual_f32, const void* y, int64_t ldy,
+                                       const void* w_post, const void* gate, int64_t ld_gate, const void* w_pre,
+                                       float residual_scale, float eps, float weight_offset, int64_t T, int64_t N,
+                                       void* d_x, int64_t ld_dx, void* d_y, int64_t ld_dy, float* d_w_pre,
+                                       float* d_w_post, void* d_gate, int64_t ld_dgate, void* scratch,
+                                       int64_t scratch_bytes, void* stream) {
+  return run_norm_backward(true, scratch, scratch_bytes, d_z, ld_dz, d_h, ld_dh, h, ldh, residual_f32, y, ldy, w_post,
+                           gate, ld_gate, w_pre, residual_scale, eps, weight_offset, T, N, d_x, ld_dx, d_y, ld_dy, d_w_pre,
+                           d_w_post, d_gate, ld_dgate, stream);
 }
 
 int silu_mul_quant_group_pack_checkpoint(const void* x, const int32_t* masked_m, int64_t E, int64_t M_max, int64_t H,
@@ -894,7 +932,7 @@ const char* fp8bs_status_string(int status) {
     case FP8BS_ERR_DEVICE: return "device is not gfx950";
     case FP8BS_ERR_LAUNCH: return "HIP call failed";
     case FP8BS_ERR_ALLOC: return "workspace allocation failed or refused during graph capture";
-    case FP8BS_ERR_SCRATCH: return "the problem needs more scratch than the static buffer of the no-allocation entry holds";
+    case FP8BS_ERR_SCRATCH: return "the problem needs more scratch than a no-allocation entry has or was given";
     default: return "unknown status";
   }
 }

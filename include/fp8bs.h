@@ -61,7 +61,7 @@ enum {
   FP8BS_ERR_DEVICE = -4, /* the current device is not gfx950                        */
   FP8BS_ERR_LAUNCH = -5, /* a HIP call failed; see fp8bs_last_hip_error()           */
   FP8BS_ERR_ALLOC = -6,  /* the split-K workspace could not be allocated            */
-  FP8BS_ERR_SCRATCH = -7 /* fp8_block_gemm_nt_preshuffled_noalloc: scratch too small */
+  FP8BS_ERR_SCRATCH = -7 /* a ..._noalloc entry point: scratch too small             */
 };
 
 /*
@@ -416,6 +416,11 @@ int moe_combine_backward(const void* d_out, int64_t ld_d, const void* y, const i
  * are taken in a fixed order: equal calls give equal bits.  Their partial sums (at most
  * 52 MB) go to the library's per-(device, stream) workspace (FP8BS_ERR_ALLOC if
  * it has to grow during HIP graph capture).  T == 0 sets the weights' gradients to zero.
+ * residual_rms_norm_backward_noalloc takes the partial sums' memory from the caller
+ * instead: at least residual_rms_norm_backward_scratch_bytes(T, N) bytes (0 for one
+ * row: scratch is not looked at), 16-byte aligned, free again for other work of the stream
+ * once the call's own is done; FP8BS_ERR_SCRATCH if it is less.  It allocates nothing and
+ * shares nothing with other calls, so a captured call replays on any stream.
  */
 int residual_rms_norm(const void* x, int64_t ldx, int32_t residual_f32, const void* y, int64_t ldy, const void* w_post,
                       const void* gate, int64_t ld_gate, const void* w_pre, float residual_scale, float eps,
@@ -427,6 +432,14 @@ int residual_rms_norm_backward(const void* d_z, int64_t ld_dz, const void* d_h, 
                                float weight_offset, int64_t T, int64_t N, void* d_x, int64_t ld_dx, void* d_y,
                                int64_t ld_dy, float* d_w_pre, float* d_w_post, void* d_gate, int64_t ld_dgate,
                                void* stream);
+int64_t residual_rms_norm_backward_scratch_bytes(int64_t T, int64_t N);
+int residual_rms_norm_backward_noalloc(const void* d_z, int64_t ld_dz, const void* d_h, int64_t ld_dh, const void* h,
+                                       int64_t ldh, int32_t residual_f32, const void* y, int64_t ldy,
+                                       const void* w_post, const void* gate, int64_t ld_gate, const void* w_pre,
+                                       float residual_scale, float eps, float weight_offset, int64_t T, int64_t N,
+                                       void* d_x, int64_t ld_dx, void* d_y, int64_t ld_dy, float* d_w_pre,
+                                       float* d_w_post, void* d_gate, int64_t ld_dgate, void* scratch,
+                                       int64_t scratch_bytes, void* stream);
 
 /*
  * silu_mul_quant_group_pack that also keeps gate and up for the backward pass in 8 bits:

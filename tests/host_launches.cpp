@@ -283,10 +283,64 @@ void one_row() {
   capturing = false;
 }
 
+// Norm backward in scratch of the caller's: nothing is allocated, the partial sums lie in it,
+// and the call does not wait for one that holds the stream's workspace.
+void given_scratch() {
+  auto run = [](int64_t T, int64_t N, void* scratch, int64_t bytes) {
+    return residual_rms_norm_backward_noalloc(at(1), N, nullptr, 0, at(2), N, 0, at(3), N, at(4), at(5), 0, at(6), 1.0f,
+                                              1e-6f, 0.0f, T, N, at(7), N, at(8), N, at<float>(9), at<float>(10),
+                                              at<float>(11), 0, scratch, bytes, stream_of(0));
+  };
+  capturing = true;
+  allocations = 0;
+  const uintptr_t scratch = reinterpret_cast<uintptr_t>(at(20));
+  for (int64_t T : {2, 300, 70000})
+    for (int64_t N : {8, 2048, 8200, 16384}) {
+      const int64_t need = residual_rms_norm_backward_scratch_bytes(T, N);
+      launches.clear();
+      int64_t blocks = 0;
+      on_launch = [&](const Launch& l) {
+        if (l.kernel.find("norm_sums_kernel") != std::string::npos) {
+          const uintptr_t from = *static_cast<uintptr_t*>(l.args[0]);
+          blocks = *static_cast<int*>(l.args[1]);
+          expect(from == scratch, "sums from elsewhere");
+          expect(int64_t(l.grid.y) * blocks * N * 4 <= need, "sums past the scratch");
+        }
+      };
+      expect(run(T, N, at(20), need) == FP8BS_OK, "refused with enough scratch");
+      on_launch = nullptr;
+      expect(launches.size() == 2 && blocks == int64_t(launches[0].grid.x) && launches[1].grid.y == 3, "launches");
+      expect(need == 3 * blocks * N * 4, "scratch is not what the sums take");
+      expect(run(T, N, at(20), need - 1) == FP8BS_ERR_SCRATCH && run(T, N, nullptr, need) == FP8BS_ERR_NULL &&
+                 run(T, N, reinterpret_cast<void*>(scratch + 8), need) == FP8BS_ERR_ALIGN, "bad scratch taken");
+    }
+  expect(allocations == 0, "an allocation");
+  expect(run(1, 2048, nullptr, 0) == FP8BS_OK, "one row refused without scratch");
+  for (int64_t N : {-8, 0, 4, 16392}) expect(residual_rms_norm_backward_scratch_bytes(300, N) == 0, "scratch of no rows");
+  expect(residual_rms_norm_backward_scratch_bytes(0, 64) == 0 && residual_rms_norm_backward_scratch_bytes(1, 64) == 0 &&
+             residual_rms_norm_backward_scratch_bytes(-1, 64) == 0, "scratch of at most one row");
+  capturing = false;
+  // from inside another call's first launch, whose thread holds the workspace
+  expect(norm_backward(300, 2048, stream_of(0)) == FP8BS_OK, "norm backward failed");
+  bool inside = false, done = false;
+  on_launch = [&](const Launch& l) {
+    if (inside) return;
+    inside = true;
+    std::thread b([&] { done = run(300, 2048, at(20), residual_rms_norm_backward_scratch_bytes(300, 2048)) == FP8BS_OK; });
+    b.join();
+  };
+  expect(norm_backward(300, 2048, stream_of(0)) == FP8BS_OK && done, "waits for the workspace");
+  on_launch = nullptr;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> scenarios = {{"threads", threads}, {"limits", limits}, {"no_columns", no_columns}, {"one_row", one_row}};
+  const std::map<std::string, void (*)()> scenarios = {{"threads", threads},
+                                                       {"limits", limits},
+                                                       {"no_columns", no_columns},
+                                                       {"one_row", one_row},
+                                                       {"given_scratch", given_scratch}};
   if (argc != 2 || scenarios.count(argv[1]) == 0) return 2;
   scenarios.at(argv[1])();
   return failed ? 1 : 0;

@@ -136,3 +136,43 @@ def test_norm_backward_of_one_row_captured_first():
         assert torch.equal(got, want) and torch.equal(a["dx"], rows[0]) and torch.equal(a["dy"], rows[1])
         norm_backward_into(norm_state(4, 1, N), torch.empty(3, N, device=DEV), torch.cuda.current_stream().cuda_stream)
         torch.cuda.synchronize()
+
+
+def binding_grads(a):
+    return F.residual_rms_norm_backward(a["dz"], a["h"], a["w"], d_h=a["dh"], y=a["y"], w_post=a["w"], gate=a["w"])
+
+
+def test_norm_backward_captured_on_a_stream_of_its_own():
+    # the partial sums of the binding's calls come from torch's allocator, so the capture is the first call there
+    a = norm_state(5, 300, 1024)
+    want = [t.clone() for t in binding_grads(a)]
+    torch.cuda.synchronize()
+    stream, graph = unused_stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = binding_grads(a)
+    for _ in range(4):
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+        binding_grads(norm_state(6, 300, 1024))
+        torch.cuda.synchronize()
+
+
+def test_replays_of_norm_backward_beside_calls_on_the_capture_stream():
+    a, b = norm_state(7, 600, 2048), norm_state(8, 600, 2048)
+    want_a, want_b = ([t.clone() for t in binding_grads(s)] for s in (a, b))
+    torch.cuda.synchronize()
+    stream, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got_a = binding_grads(a)
+    for _ in range(20):
+        with torch.cuda.stream(other):
+            graph.replay()
+        with torch.cuda.stream(stream):
+            got_b = binding_grads(b)
+        torch.cuda.synchronize()
+        for g, w in zip((*got_a, *got_b), (*want_a, *want_b)):
+            assert torch.equal(g, w)

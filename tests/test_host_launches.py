@@ -43,3 +43,7 @@ def test_combine_backward_without_columns(program):
 
 def test_norm_backward_of_one_row_allocates_nothing(program):
     run(program, "one_row")
+
+
+def test_norm_backward_in_scratch_of_the_callers(program):
+    run(program, "given_scratch")
