@@ -115,3 +115,167 @@ def test_route_backward_of_contiguous_rows(T, E, k, scoring, renormalize, dtype)
             assert (np.abs(view.double().cpu().numpy() - ref) <= bound).all()
         else:
             assert torch.equal(view, got)
+
+
+# ------------------------------------------------------------------ norms: several rows a workgroup
+
+
+def between_roundings(got, ref, err, what):
+    """got bf16 lies between the roundings of ref - err and ref + err (rounding is monotonic)."""
+    lo, hi = (ref - err).to(BF), (ref + err).to(BF)
+    bad = ~((got >= lo) & (got <= hi))
+    assert not bad.any(), "%s: %d of %d off, first at %s" % (what, bad.sum(), bad.numel(), bad.nonzero()[0].tolist())
+
+
+def within(got, ref, err, what):
+    bad = ~((got.double() - ref).abs() <= err)
+    assert not bad.any(), "%s: %d of %d off, first at %s" % (what, bad.sum(), bad.numel(), bad.nonzero()[0].tolist())
+
+
+def output(got, ref, err, what):
+    (between_roundings if got.dtype == BF else within)(got, ref, err, what)
+
+
+def depth(N):
+    """Additions on the way of one of N terms of a row: a thread's 8 or 16, lanes (4 + 2), wavefronts (4)."""
+    return (8 if N <= 8192 else 16) + 10
+
+
+def inv_rel(N):
+    """1 / sqrt(mean square + eps): half of the sum's, the mean's (2) and eps' (1) roundings, and two ulps of its own."""
+    return ((depth(N) + 3) / 2 + 2) * U
+
+
+def rows_of(seed, T, N, gate, res):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def r(*shape, dtype=BF):
+        return torch.randn(shape, generator=g, device=DEV).to(dtype)
+    # rows of unequal magnitudes: one taken for another does not go unnoticed
+    size = torch.exp(torch.randn(T, 1, generator=g, device=DEV))
+    return dict(x=(r(T, N, dtype=torch.float32) * 2 * size).to(res), y=(r(T, N, dtype=torch.float32) * size.flip(0)).to(BF),
+                w_pre=1 + 0.2 * r(N), w_post=1 + 0.2 * r(N), gate=r(T, N) if gate == "full" else r(N) if gate else None,
+                dz=r(T, N), dh=r(T, N, dtype=res))
+
+
+MANY_ROWS = [  # T past three rows for each workgroup of the grid: with an odd remainder where T is
+    (6145, 520), (3073, 2048), (769, 5120), (769, 7168), (771, 16384), (770, 8200)]
+KINDS = [(BF, "channel", True), (torch.float32, "full", True), (torch.float32, "channel", False), (BF, None, True),
+         (torch.float32, "before", False), (BF, "full", False)]
+
+
+def parts(a, gate, post):
+    kw = dict(y=None if gate == "before" else a["y"], w_post=a["w_post"] if post else None,
+              gate=None if gate == "before" else a["gate"])
+    return kw, (lambda rows: {n: t[rows] if t is not None and t.dim() == 2 else t for n, t in kw.items()})
+
+
+@pytest.mark.parametrize("T,N", MANY_ROWS)
+@pytest.mark.parametrize("res,gate,post", KINDS)
+def test_norm_of_many_rows(T, N, res, gate, post):
+    a = rows_of(T + N, T, N, gate, res)
+    kw, part_of = parts(a, gate, post)
+    out = "both" if N % 128 == 0 else "bf16"
+    opts = dict(residual_scale=0.75, eps=1e-5, out=out)
+    h, z, q, sf = F.residual_rms_norm(a["x"], a["w_pre"], **kw, **opts)
+    again = F.residual_rms_norm(a["x"], a["w_pre"], **kw, **opts)
+    assert torch.equal(h, again[0]) and torch.equal(z, again[1])
+    # the same bits as calls in which no workgroup has a second row
+    for t in range(0, T, 256):
+        rows = slice(t, min(T, t + 256))
+        n = rows.stop - t
+        h1, z1, q1, sf1 = F.residual_rms_norm(a["x"][rows], a["w_pre"], **part_of(rows), **opts)
+        assert torch.equal(h[rows], h1) and torch.equal(z[rows], z1), "rows from %d" % t
+        if q is not None:
+            assert torch.equal(q[rows], q1) and torch.equal(sf[:, rows], sf1[:, :n]), "rows from %d" % t
+    # 64 bits
+    x, w_pre = a["x"].double(), a["w_pre"].double()
+    b = torch.zeros_like(x)
+    if gate != "before":
+        b = a["y"].double()
+        if post:
+            b = b * torch.rsqrt(b.square().mean(1, keepdim=True) + 1e-5) * a["w_post"].double()
+        if a["gate"] is not None:
+            b = b * a["gate"].double()
+    href = 0.75 * x + b
+    # b: its row's factor, the weights' two products, the products with y and a gate of the token; then one of h
+    herr = (inv_rel(N) + 5 * U) * b.abs() + U * href.abs()
+    output(h, href, herr, "h")
+    inv = torch.rsqrt(href.square().mean(1, keepdim=True) + 1e-5)
+    # h's errors move its root mean square by their own at most; the factor times the weight, and the product
+    rel = herr.norm(dim=1, keepdim=True) / href.norm(dim=1, keepdim=True) + inv_rel(N) + 3 * U
+    zref = href * inv * w_pre
+    zerr = (herr + rel * href.abs()) * inv * w_pre.abs() * (1 + 1e-4)
+    between_roundings(z, zref, zerr, "z")
+    if q is not None:  # (every 37th row: the rest has the bits of short calls)
+        some = torch.arange(T - 1, -1, -37, device=DEV)
+        R.check_quantized(zref[some].cpu().numpy(), q[some].cpu().numpy(), sf[:, some].cpu().numpy(), zerr[some].cpu().numpy())
+
+
+BACKWARD_ROWS = [(2305, 520), (705, 2048), (700, 7168), (4099, 256), (515, 16384), (513, 8200)]
+
+
+@pytest.mark.parametrize("T,N", BACKWARD_ROWS)
+@pytest.mark.parametrize("res,gate,post", KINDS)
+def test_norm_backward_of_many_rows(T, N, res, gate, post):
+    a = rows_of(T * N, T, N, gate, res)
+    kw, part_of = parts(a, gate, post)
+    opts = dict(residual_scale=0.75, eps=1e-5)
+    got = F.residual_rms_norm_backward(a["dz"], a["x"], a["w_pre"], d_h=a["dh"], **kw, **opts)
+    for g1, g2 in zip(got, F.residual_rms_norm_backward(a["dz"], a["x"], a["w_pre"], d_h=a["dh"], **kw, **opts)):
+        assert g1 is None and g2 is None or torch.equal(g1, g2)
+    for t in range(0, T, 256):  # (a grid has at least 256 workgroups where there are as many rows)
+        rows = slice(t, min(T, t + 256))
+        one = F.residual_rms_norm_backward(a["dz"][rows], a["x"][rows], a["w_pre"], d_h=a["dh"][rows], **part_of(rows), **opts)
+        for name, g, g1 in zip(("d_x", "d_y", "", "", "d_gate"), got, one):
+            if name and g is not None and g.dim() == 2:
+                assert torch.equal(g[rows], g1), "%s, rows from %d" % (name, t)
+    # 64 bits.  Sums of a row as above; a product and its weight add 2 roundings to each term of the inner products
+    h, dz, dh_in, w_pre = a["x"].double(), a["dz"].double(), a["dh"].double(), a["w_pre"].double()
+    mean = lambda t: t.mean(1, keepdim=True)  # noqa: E731
+    rh = torch.rsqrt(mean(h * h) + 1e-5)
+    hh, u = h * rh, dz * w_pre
+    m, m_abs = mean(u * hh), mean((u * hh).abs())
+    m_err = (depth(N) + 6) * U * m_abs + inv_rel(N) * m.abs()
+    dh = dh_in + rh * (u - hh * m)
+    # u, hh * m, their difference, the factor, the sum
+    dh_err = rh * ((inv_rel(N) + 4 * U) * u.abs() + hh.abs() * (m_err + (2 * inv_rel(N) + 4 * U) * m.abs())) + U * dh.abs()
+    slack = 1 + 1e-4  # terms of u^2
+    output(got[0], 0.75 * dh, (0.75 * dh_err + U * dh.abs()) * slack, "d_x")
+    # sums over the tokens: a workgroup's rows one after the other (at most 16 here), then one in sixteen of the
+    # workgroups' sums (of at most 512 here), then sixteen
+    rows_depth = 16 + 512 // 16 + 16
+    over_rows = lambda t, err: (t.sum(0), (err.sum(0) + rows_depth * U * t.abs().sum(0)) * slack)  # noqa: E731
+    t = dz * hh
+    within(got[2], *over_rows(t, (inv_rel(N) + 2 * U) * t.abs()), "d_w_pre")
+    if gate == "before":
+        assert got[1] is None and got[3] is None and got[4] is None
+        return
+    y = a["y"].double()
+    gt = torch.ones_like(y) if a["gate"] is None else a["gate"].double() * torch.ones_like(y)
+    db, db_err = dh * gt, dh_err * gt.abs() + U * (dh * gt).abs()
+    yh, wp, ry_rel = y, torch.ones_like(w_pre), 0.0
+    if post:
+        wp, ry_rel = a["w_post"].double(), inv_rel(N)
+        ry = torch.rsqrt(mean(y * y) + 1e-5)
+        yh = y * ry
+        v = db * wp
+        m, m_abs = mean(v * yh), mean((v * yh).abs())
+        m_err = mean((db_err * wp * yh).abs()) + (depth(N) + 8) * U * m_abs + ry_rel * m.abs()
+        dy = ry * (v - yh * m)
+        dy_err = ry * (db_err * wp.abs() + (ry_rel + 4 * U) * v.abs() + yh.abs() * (m_err + (2 * ry_rel + 4 * U) * m.abs()))
+        output(got[1], dy, (dy_err + U * dy.abs()) * slack, "d_y")
+        t = db * yh
+        within(got[3], *over_rows(t, db_err * yh.abs() + (ry_rel + 2 * U) * t.abs()), "d_w_post")
+    else:
+        assert got[3] is None
+        output(got[1], db, db_err * slack, "d_y")
+    if a["gate"] is None:
+        assert got[4] is None
+        return
+    t = dh * yh * wp
+    err = dh_err * (yh * wp).abs() + (ry_rel + 3 * U) * t.abs()
+    if a["gate"].dim() == 1:
+        within(got[4], *over_rows(t, err), "d_gate")
+    else:
+        output(got[4], t, err * slack, "d_gate")
