@@ -200,11 +200,11 @@ __global__ __launch_bounds__(256) void silu_backward_kernel(const uint16_t* __re
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float gate = g[i] * sg, u = up[i] * su;
-      const float ex = expf(-gate);
-      const float sig = __builtin_amdgcn_rcpf(1.0f + ex);
-      // 1 - s = e^-g s, without the cancellation; at gates so low that e^-g overflows s is 0
-      // and both gradients are 0
-      const float rest = ex < 3e38f ? ex * sig : 1.0f;
+      // s and 1 - s from e^-|g| <= 1: 1 / (1 + e^-|g|) and e^-|g| times that, without the
+      // cancellation, and small only where they are (the reciprocal of 1 + e^88 would be 0)
+      const float ex = expf(-__builtin_fabsf(gate));
+      const float r = __builtin_amdgcn_rcpf(1.0f + ex), re = r * ex;
+      const float sig = gate < 0.0f ? re : r, rest = gate < 0.0f ? r : re;
       dg[i] = d[i] * u * sig * __builtin_fmaf(gate, rest, 1.0f);
       du[i] = d[i] * gate * sig;
     }

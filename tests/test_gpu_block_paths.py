@@ -279,3 +279,89 @@ def test_norm_backward_of_many_rows(T, N, res, gate, post):
         within(got[4], *over_rows(t, err), "d_gate")
     else:
         output(got[4], t, err * slack, "d_gate")
+
+
+# ------------------------------------------------------------------ checkpoint: several units a wavefront
+
+# experts, rows an expert, columns: past three (row, 512 columns) units for each of the grid's 7168 wavefronts, with
+# experts that are empty, full, over-full and ragged
+UNITS = [(37, 700, 640), (19, 699, 2048), (90, 501, 128)]
+
+
+def many_units(E, M, H):
+    g = gen(3, E, M)
+    counts = g.integers(0, M + 1, E)
+    counts[[0, 5, 6, E - 1]] = 0, M, M + 9, -3
+    counts[7:] = np.where(g.random(E - 7) < 0.8, np.maximum(counts[7:], M - 40), counts[7:])
+    valid = torch.from_numpy(np.arange(M) < np.clip(counts, 0, M)[:, None]).to(DEV)
+    assert int(valid.sum()) * -(-H // 512) > 3 * 7168
+    t = torch.Generator(device=DEV).manual_seed(E)
+    size = torch.exp(torch.randn(E, M, 1, generator=t, device=DEV))
+    x = (torch.randn(E, M, 2 * H, generator=t, device=DEV) * size).to(BF)
+    x[~valid] = float("nan")
+    return torch.from_numpy(counts).int().to(DEV), valid, x, t
+
+
+def padding(*shape, dtype=torch.uint8):
+    return torch.full(shape, 0x2B if dtype == torch.uint8 else -7, dtype=dtype, device=DEV)
+
+
+def values(codes, words, groups):
+    """Values of codes [E, M, 128 * groups] at the UE8M0 bytes of words [E, ceil(groups / 4), M], in 64 bits."""
+    E, W, M = words.shape
+    b = words.view(torch.uint8).view(E, W, M, 4).transpose(1, 2).reshape(E, M, 4 * W)[..., :groups]
+    return codes.view(torch.float8_e4m3fn).double() * torch.exp2(b.double() - 127).repeat_interleave(128, dim=-1)
+
+
+@pytest.mark.parametrize("E,M,H", UNITS)
+def test_checkpoint_of_many_units(E, M, H):
+    m, valid, x, _ = many_units(E, M, H)
+    W = -(-H // 512)
+    new = lambda: [padding(E, M, H), padding(E, W, M, dtype=torch.int32),  # noqa: E731
+                   padding(E, M, 2 * H), padding(E, 2 * W, M, dtype=torch.int32)]
+    q, sf, cq, csf = F.silu_mul_quant_group_pack_checkpoint(x, m, *new())
+    for a, b in zip((q, sf, cq, csf), F.silu_mul_quant_group_pack_checkpoint(x, m, *new())):
+        assert torch.equal(a, b)
+    q2, sf2 = F.silu_mul_quant_group_pack(x, m, q=padding(E, M, H), sf=padding(E, W, M, dtype=torch.int32))
+    assert torch.equal(q, q2) and torch.equal(sf, sf2)
+    assert (cq[~valid] == 0x2B).all() and (csf.transpose(1, 2)[~valid] == -7).all()
+    for half in (0, 1):  # each half value for value as a quantization of its own
+        rq, rsf = F.fp8_quant_group_pack(x[..., half * H:(half + 1) * H].reshape(E * M, H).contiguous())
+        assert torch.equal(cq[..., half * H:(half + 1) * H][valid], rq.view(E, M, H)[valid])
+        rows = csf[:, half * W:(half + 1) * W].transpose(1, 2)[valid]
+        assert torch.equal(rows, rsf[:, :E * M].t().reshape(E, M, W)[valid])
+
+
+@pytest.mark.parametrize("E,M,H", UNITS)
+def test_checkpoint_backward_of_many_units(E, M, H):
+    m, valid, x, t = many_units(E, M, H)
+    W, W2 = -(-H // 512), -(-2 * H // 512)
+    _, _, cq, csf = F.silu_mul_quant_group_pack_checkpoint(x, m)
+    d = torch.randn(E, M, H, generator=t, device=DEV).to(BF)
+    d[~valid] = float("nan")
+    dx = F.silu_mul_backward_from_checkpoint(d, m, cq, csf, d_x=torch.full_like(x, float("nan")))
+    q, sf = F.silu_mul_backward_from_checkpoint(d, m, cq, csf, quantize=True, q=padding(E, M, 2 * H),
+                                                sf=padding(E, W2, M, dtype=torch.int32))
+    assert dx[~valid].isnan().all() and (q[~valid] == 0x2B).all() and (sf.transpose(1, 2)[~valid] == -7).all()
+    # the same bits as an expert alone, where no wavefront has a second unit
+    for e in range(E):
+        one = slice(e, e + 1)
+        n = int(valid[e].sum())
+        assert n * W <= 7168
+        dx1 = F.silu_mul_backward_from_checkpoint(d[one], m[one], cq[one], csf[one])
+        assert torch.equal(dx[e, :n], dx1[0, :n]), "expert %d" % e
+        q1, sf1 = F.silu_mul_backward_from_checkpoint(d[one], m[one], cq[one], csf[one], quantize=True)
+        assert torch.equal(q[e, :n], q1[0, :n]) and torch.equal(sf[e, :, :n], sf1[0, :, :n]), "expert %d" % e
+    # 64 bits
+    groups = H // 128
+    cs = csf.view(E, 2, W, M)
+    gate = values(cq[..., :H].contiguous(), cs[:, 0].contiguous(), groups)[valid]
+    up = values(cq[..., H:].contiguous(), cs[:, 1].contiguous(), groups)[valid]
+    s, rest, dv = torch.sigmoid(gate), torch.sigmoid(-gate), d[valid].double()
+    ref = torch.cat([dv * up * s * (1 + gate * rest), dv * gate * s], -1)
+    # exp of a rounded argument, reciprocal, four products: 16 roundings, of 1 + |gate| (1 - s) where gates are negative
+    err = 16 * U * torch.cat([(dv * up).abs() * s * (1 + gate.abs() * rest), (dv * gate).abs() * s], -1) + 1e-36
+    between_roundings(dx[valid], ref, err, "d_x")
+    some = torch.arange(ref.shape[0] - 1, -1, -37, device=DEV)
+    rows = sf.transpose(1, 2)[valid][some].t().contiguous()
+    R.check_quantized(ref[some].cpu().numpy(), q[valid][some].cpu().numpy(), rows.cpu().numpy(), err[some].cpu().numpy())
