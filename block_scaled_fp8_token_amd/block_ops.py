@@ -4,6 +4,11 @@ stream, and the 8-bit checkpoint of the gated activation, each with its backward
 Binding of the entry points of the same names in include/fp8bs.h (which states the
 formulas).  Wrong types, shapes and strides raise TypeError or ValueError before
 anything is launched; all tensors of a call lie on the current device.
+
+The calls take tensors for their values: as everywhere in this binding, nothing is recorded for
+automatic differentiation and results do not require a gradient, whatever the inputs say.  A
+training step calls the backward entry points itself, or wraps a pair of calls in a
+torch.autograd.Function.  Outputs that a caller passes must not overlap inputs (not checked).
 """
 from __future__ import annotations
 

@@ -17,7 +17,8 @@
 //
 // Measured, 32768 valid rows of H = 2048 in 32 experts: forward 92.5 us, 471 MB, 5.1 TB/s (it
 // issues about 250 vector instructions a unit, three quarters of the time that memory
-// takes); backward to bf16 99 us, 538 MB, 5.4 TB/s.  A copy of 400 MB reaches 5.4 TB/s.
+// takes); backward to bf16 99 us, 538 MB, 5.4 TB/s, to codes 81 us, 405 MB, 5.0 TB/s.  A copy of
+// 400 MB reaches 5.4 TB/s.
 // Before: waiting for each unit's own loads 108 and 116 us, and a contiguous run of units
 // for each wavefront 118 us forward.
 #include "block_device.hpp"

@@ -11,7 +11,7 @@
 // Measured, 8 pairs of 7168 columns a token: 4096 tokens forward with a base 93.7 us, 581
 // MB, 6.2 TB/s (114 us without the streaming policy on the rows and the result); 2048
 // tokens backward with codes and weights' gradients 75.5 us, 378 MB, 5.0 TB/s (85 us without
-// it; 94 us with one pair at a time and a barrier for each).
+// it; 94 us with one pair at a time and a barrier for each), to bf16 95.5 us, 492 MB, 5.15 TB/s.
 #include "block_device.hpp"
 #include "block_launch.hpp"
 

@@ -15,10 +15,12 @@
 // Bound by vector instructions (about 1350 in a wavefront for four tokens; the memory would
 // take 2 us below) and, for few tokens, by the length of their chain.  Measured in a graph,
 // bf16 logits, 16384 tokens, 256 experts: 8 chosen in 4 of 8 groups by biased sigmoid scores
-// 11.3 us, 8 by softmax 7.1 us; 9 chosen, which the second kernel takes, 18 us (it took 36
-// us for the 8 in groups).  512 experts: 8 chosen 15.9 and 10.0 us, 9 chosen 27 us.  One token of
-// 256: 5.6 and 3.6 us.  Backward, softmax not renormalised: 11.1 us, 14.9 us with a memory
-// instruction for every 64 logits and a comparison of every choice with every expert.
+// 11.3 us, 8 by softmax 7.1 us; 9 chosen, which the second kernel takes, 18 us, in groups 38 us
+// (8 in groups 36).  512 experts: 8 chosen 15.9 and 10.0 us, 9 chosen 27 us, 10 chosen 32 us.
+// One token of 256: 5.6 and 3.6 us.  Backward, softmax not renormalised: 11.1 us, 14.9 us with
+// a memory instruction for every 64 logits and a comparison of every choice with every expert;
+// with inputs past the caches 13.0 us, and 10.5 us for the forms whose gradients stay at the
+// chosen experts.
 #include <type_traits>
 
 #include "block_device.hpp"

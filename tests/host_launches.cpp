@@ -142,7 +142,7 @@ void threads() {
   Call calls[] = {{"norm backward", [](void* s) { return norm_backward(512, 2048, s); }, 0},
                   {"quantization into the experts' layout", to_experts, 0},
                   {"split GEMM", split_gemm, 0}};
-  for (int round = 0; round < 2; ++round)  // the first round allocates, which clears the counters with a launch
+  for (int turn = 0; turn < 2; ++turn)  // the first allocates, which clears the counters with a launch
     for (Call& c : calls)
       for (int s = 0; s < 2; ++s) {
         launches.clear();
