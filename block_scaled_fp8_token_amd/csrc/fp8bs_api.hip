@@ -123,18 +123,19 @@ int get_workspace(size_t need, hipStream_t stream, void** out, std::unique_lock<
 // code never uses the array's name as an address: its device address comes from
 // hipGetSymbolAddress, once per device, with that device current.  The arrival
 // counters at its front are cleared by a fill kernel on the first call's stream;
-// every call leaves them at zero.  All calls on one GPU share it.
+// every call leaves them at zero.  All calls on one GPU share it, each holding the mutex until
+// its last launch, as with a workspace.
 constexpr size_t kStaticScratchBytes = size_t(8) << 20;
 static __device__ __align__(256) unsigned char scratch[kStaticScratchBytes];
 
-int static_scratch(hipStream_t stream, void** out) {
+int static_scratch(hipStream_t stream, void** out, std::unique_lock<std::mutex>* held) {
   static std::mutex mu;
   static std::map<int, void*> ptrs;
   *out = nullptr;
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail_hip(e);
-  std::lock_guard<std::mutex> lk(mu);
+  *held = std::unique_lock<std::mutex>(mu);
   auto it = ptrs.find(dev);
   if (it == ptrs.end()) {
     void* ptr = nullptr;
@@ -560,8 +561,9 @@ int fp8_block_gemm_nt_preshuffled_noalloc(const void* a, const uint32_t* sfa, in
   const size_t need = fp8bs::gemm_workspace_bytes(p, cfg);
   if (need > kStaticScratchBytes) return FP8BS_ERR_SCRATCH;
   void* ws = nullptr;
+  std::unique_lock<std::mutex> held;
   if (need > 0) {
-    st = static_scratch(static_cast<hipStream_t>(stream), &ws);
+    st = static_scratch(static_cast<hipStream_t>(stream), &ws, &held);
     if (st != FP8BS_OK) return st;
   }
   hipError_t e = fp8bs::launch_gemm(p, cfg, ws, static_cast<hipStream_t>(stream));

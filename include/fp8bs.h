@@ -220,8 +220,9 @@ int fp8_block_gemm_nt_preshuffled(const void* a, const uint32_t* sfa, int64_t ld
  * (arrival counters and fp32 partials) is a static device array of 8 MiB per GPU
  * instead of the per-stream workspace, so this call never allocates or frees.  For
  * M <= 64 and K <= 143360 (the weight-streaming kernel) the automatic configuration
- * needs at most 64 KiB + 224 * 64 * 128 * 4 bytes (7.4 MB), for larger M none; a
- * problem needing more than 8 MiB returns FP8BS_ERR_SCRATCH without launching.  Every call on one GPU shares that array:
+ * needs at most 64 KiB + 224 * 64 * 128 * 4 bytes (7.4 MB), for larger M none where the
+ * tiles fill the GPU (else K is split there too); a problem needing more than 8 MiB
+ * returns FP8BS_ERR_SCRATCH without launching.  Every call on one GPU shares that array:
  * calls that overlap on one GPU (different streams, or a graph replay running
  * beside another call) race and give undefined results.  The first call on a device
  * clears the counters with a fill kernel on its stream; every call leaves them clear.

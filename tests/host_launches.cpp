@@ -126,8 +126,45 @@ int to_experts(void* stream) {
   return fp8_quant_group_pack_to_experts(at(1), 512, 4096, 512, at<int32_t>(2), 8, 32, 64, at(3), at<uint32_t>(4),
                                          at<int32_t>(5), at<int32_t>(6), stream);
 }
+int noalloc_gemm(void* stream) {
+  return fp8_block_gemm_nt_preshuffled_noalloc(at(1), at<uint32_t>(2), 512, at(3), at<float>(4), at(5), 960, 512, 960,
+                                               18432, stream);
+}
 int split_gemm(void* stream) {
   return fp8_block_gemm_nt(at(1), at<uint32_t>(2), 64, at(3), at<float>(4), at(5), 7168, 64, 7168, 18432, stream);
+}
+
+// The entry that allocates nothing has one scratch for the GPU: its calls on one stream do not
+// break into each other either.
+void noalloc_threads() {
+  expect(noalloc_gemm(stream_of(0)) == FP8BS_OK, "GEMM without allocation failed");  // clears the counters
+  launches.clear();
+  std::mutex m;
+  std::condition_variable cv;
+  bool started = false, answered = false;
+  on_launch = [&](const Launch&) {
+    std::unique_lock<std::mutex> lk(m);
+    if (!started) {
+      started = true;
+      cv.notify_all();
+      cv.wait_for(lk, std::chrono::milliseconds(100), [&] { return answered; });
+    } else {
+      answered = true;
+      cv.notify_all();
+    }
+  };
+  std::thread a([&] { expect(noalloc_gemm(stream_of(0)) == FP8BS_OK, "GEMM without allocation failed"); });
+  std::thread b([&] {
+    std::unique_lock<std::mutex> lk(m);
+    cv.wait(lk, [&] { return started; });
+    lk.unlock();
+    expect(noalloc_gemm(stream_of(0)) == FP8BS_OK, "GEMM without allocation failed");
+  });
+  a.join();
+  b.join();
+  on_launch = nullptr;
+  expect(launches.size() == 4 && launches[0].by == launches[1].by && launches[2].by == launches[3].by,
+         "a GEMM without allocation breaks into another");
 }
 
 // A call whose launches share the stream's workspace is not broken into by another host
@@ -337,6 +374,7 @@ void given_scratch() {
 
 int main(int argc, char** argv) {
   const std::map<std::string, void (*)()> scenarios = {{"threads", threads},
+                                                       {"noalloc_threads", noalloc_threads},
                                                        {"limits", limits},
                                                        {"no_columns", no_columns},
                                                        {"one_row", one_row},

@@ -33,6 +33,10 @@ def test_threads_on_one_stream(program):
     run(program, "threads")
 
 
+def test_threads_on_the_scratch_of_the_entry_that_allocates_nothing(program):
+    run(program, "noalloc_threads")
+
+
 def test_largest_sizes(program):
     run(program, "limits")
 
