@@ -543,7 +543,8 @@ hipError_t launch_norm(const NormProblem& p, const void* x, int64_t ldx, void* h
       const unsigned threads = threads_for(p.N, ch.value);
       // sixteen wavefronts on each compute unit (8192 x 7168: 79 us with one workgroup of
       // fourteen there, 82 with two, 121 with a workgroup for every row, before the last steps;
-      // 85 where each had a contiguous run of the rows)
+      // 85 where each had a contiguous run of the rows).  Rounded down: rows of 4104 to 7680
+      // columns have one workgroup of nine to fifteen (8192 x 5120 to codes: 56.7 us, 5.2 TB/s)
       const int64_t fit = (int64_t)kCUs * (1024 / threads);
       hipLaunchKernelGGL((norm_kernel<f32.value, full.value, quant.value, ch.value>),
                          dim3((unsigned)(p.T < fit ? p.T : fit)), dim3(threads), 0, stream, p,
