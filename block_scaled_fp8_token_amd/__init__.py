@@ -29,6 +29,8 @@ __all__ = [
     "fp8_block_gemm_nt_preshuffled_noalloc", "check_dense_shapes", "check_masked_shapes", "check_contiguous_shapes",
     "moe_route_topk", "moe_route_topk_backward", "moe_combine", "moe_combine_backward", "residual_rms_norm",
     "residual_rms_norm_backward", "silu_mul_quant_group_pack_checkpoint", "silu_mul_backward_from_checkpoint",
+    "moe_decode_layer", "moe_decode_layer_preshuffled", "moe_decode_layer_w4", "w4_group_quant", "w4_preshuffle",
+    "w4_group_gemv_nt",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +87,12 @@ _SIGS = {
                                            _F32, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P],
     "silu_mul_quant_group_pack_checkpoint": [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P],
     "silu_mul_backward_from_checkpoint": [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P],
+    "moe_decode_layer_scratch_bytes": [_I64, _I32, _I64],
+    **{_n: [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]
+       for _n in ("moe_decode_layer", "moe_decode_layer_preshuffled", "moe_decode_layer_w4")},
+    "w4_group_quant": [_P, _I64, _I64, _I32, _I32, _P, _P, _P, _P],
+    "w4_preshuffle": [_P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P],
+    "w4_group_gemv_nt": [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _I64, _P],
     "fp8bs_gemm_config_count": [],
     "fp8bs_gemm_config": [ctypes.c_int, _I64, _I64, _I64, _I32P, _I32P, _I32P, _I32P],
     "fp8bs_gemm_config_of": [_I32, ctypes.c_int, _I64, _I64, _I64, _I32, _I32P, _I32P, _I32P],
@@ -99,7 +107,7 @@ for _name, _args in _SIGS.items():
                           "`python block_scaled_fp8_token_amd/build.py`" % _name) from None
     _fn.argtypes = _args
     _fn.restype = {"fp8bs_status_string": ctypes.c_char_p,
-                   "residual_rms_norm_backward_scratch_bytes": _I64}.get(_name, ctypes.c_int)
+                   "residual_rms_norm_backward_scratch_bytes": _I64, "moe_decode_layer_scratch_bytes": _I64}.get(_name, ctypes.c_int)
 
 
 class Fp8bsError(RuntimeError):
@@ -641,3 +649,6 @@ def gemm_config(masked, M: int, N: int, K: int) -> dict:
 from .block_ops import (  # noqa: E402
     moe_combine, moe_combine_backward, moe_route_topk, moe_route_topk_backward, residual_rms_norm,
     residual_rms_norm_backward, silu_mul_backward_from_checkpoint, silu_mul_quant_group_pack_checkpoint)
+from .decode_ops import (  # noqa: E402
+    moe_decode_layer, moe_decode_layer_preshuffled, moe_decode_layer_w4, w4_group_gemv_nt, w4_group_quant, w4_preshuffle,
+)

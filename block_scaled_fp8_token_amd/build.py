@@ -18,7 +18,7 @@ OUT = os.path.join(HERE, "libfp8bs.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["quant_kernels.hip", "gemm_kernels.hip", "route_kernels.hip", "combine_kernels.hip", "norm_kernels.hip",
-           "checkpoint_kernels.hip", "fp8bs_api.hip"]
+           "checkpoint_kernels.hip", "moe_decode_kernels.hip", "w4_kernels.hip", "fp8bs_api.hip"]
 
 # Packed-fp32 VALU forms are switched off for every kernel: ordinary scalar
 # fp32 code is what the kernels are written in.

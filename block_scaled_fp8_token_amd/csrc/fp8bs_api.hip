@@ -13,6 +13,7 @@
 
 #include "../../include/fp8bs.h"
 #include "block_launch.hpp"
+#include "decode_launch.hpp"
 #include "fp8bs_launch.hpp"
 
 namespace {
@@ -394,6 +395,61 @@ int check_checkpoint(int64_t E, int64_t M_max, int64_t H) {
   if (E < 0 || E > fp8bs::kCheckpointMaxE || M_max < 0 || H < 0 || H % 128 != 0) return FP8BS_ERR_SHAPE;
   if (M_max > INT32_MAX || E * M_max > INT32_MAX || H > (1 << 28)) return FP8BS_ERR_SHAPE;
   return E == 0 || M_max == 0 || H == 0 ? 1 : FP8BS_OK;
+}
+
+int run_moe_decode(fp8bs::Weights kind, const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf,
+                   const int32_t* topk_ids, const float* weights, const void* w13, const void* s13, const void* w2,
+                   const void* s2, const void* base, int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t K,
+                   int64_t H, void* out, int64_t ld_out, void* scratch, int64_t scratch_bytes, void* stream) {
+  if (T < 0 || T > fp8bs::kMoeDecodeMaxT || topk < 1 || topk > fp8bs::kMoeDecodeMaxTopk || E < 1 ||
+      E > fp8bs::kMoeDecodeMaxE || K < 128 || K % 128 != 0 || K > fp8bs::kMoeDecodeMaxK || H < 128 || H % 128 != 0 ||
+      H > fp8bs::kMoeDecodeMaxK)
+    return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!q || !sf || !topk_ids || !weights || !w13 || !s13 || !w2 || !s2 || !out || !scratch) return FP8BS_ERR_NULL;
+  // the kernels' 32-bit offsets
+  const int64_t words = (K + 511) / 512, most = INT64_C(1) << 31;
+  if (ldq < K || ldq >= most || (T - 1) * ldq + K >= most || ld_sf < T || ld_sf >= most ||
+      ((words - 1) * ld_sf + T) * 4 >= most || bad_rows(base, ld_base, K) || ld_out < K)
+    return FP8BS_ERR_SHAPE;
+  const uintptr_t scales = kind == fp8bs::Weights::kW4 ? 16 : 4;
+  if (!aligned(q, 16) || ldq % 16 != 0 || !aligned(sf, 4) || !aligned(topk_ids, 4) || !aligned(weights, 4) ||
+      !aligned(w13, 16) || !aligned(s13, scales) || !aligned(w2, 16) || !aligned(s2, scales) ||
+      misaligned_rows(base, ld_base) || misaligned_rows(out, ld_out) || !aligned(scratch, 16))
+    return FP8BS_ERR_ALIGN;
+  if (scratch_bytes < (int64_t)fp8bs::moe_decode_scratch_bytes(T, topk, H)) return FP8BS_ERR_SCRATCH;
+  int st = check_device();
+  if (st != FP8BS_OK) return st;
+  fp8bs::MoeDecodeProblem p;
+  p.q = static_cast<const uint8_t*>(q);
+  p.sf = sf;
+  p.ids = topk_ids;
+  p.weights = weights;
+  p.w13 = static_cast<const uint8_t*>(w13);
+  p.s13 = s13;
+  p.w2 = static_cast<const uint8_t*>(w2);
+  p.s2 = s2;
+  p.base = static_cast<const uint16_t*>(base);
+  p.out = static_cast<uint16_t*>(out);
+  p.ldq = ldq;
+  p.ld_sf = ld_sf;
+  p.ld_base = ld_base;
+  p.ld_out = ld_out;
+  p.T = (int)T;
+  p.topk = topk;
+  p.E = (int)E;
+  p.K = (int)K;
+  p.H = (int)H;
+  hipError_t e = fp8bs::launch_moe_decode(p, kind, scratch, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+// Format, group and sizes of 4-bit weights; FP8BS_OK or the status.
+int check_w4(int64_t rows, int64_t K, int32_t format, int32_t group, const void* zeros) {
+  if (rows < 0 || rows > (INT64_C(1) << 40) || K < 128 || K % 128 != 0 || K > fp8bs::kW4MaxK) return FP8BS_ERR_SHAPE;
+  if (format == FP8BS_E2M1) return group == 32 && !zeros ? FP8BS_OK : FP8BS_ERR_SHAPE;
+  if (format != FP8BS_INT4 || (group != 32 && group != 64 && group != 128)) return FP8BS_ERR_SHAPE;
+  return FP8BS_OK;
 }
 
 }  // namespace
@@ -891,6 +947,103 @@ int silu_mul_backward_from_checkpoint(const void* d_y, const int32_t* masked_m, 
   hipError_t e = fp8bs::launch_silu_backward(static_cast<const uint16_t*>(d_y), masked_m, E, M_max, H,
                                              static_cast<const uint8_t*>(cq), csf, static_cast<uint16_t*>(d_x),
                                              static_cast<uint8_t*>(q), sf, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int64_t moe_decode_layer_scratch_bytes(int64_t T, int32_t topk, int64_t H) {
+  if (T < 1 || T > fp8bs::kMoeDecodeMaxT || topk < 1 || topk > fp8bs::kMoeDecodeMaxTopk || H < 1 ||
+      H > fp8bs::kMoeDecodeMaxK)
+    return 0;
+  return (int64_t)fp8bs::moe_decode_scratch_bytes(T, topk, H);
+}
+
+int moe_decode_layer(const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf, const int32_t* topk_ids,
+                     const float* weights, const void* w13, const float* s13, const void* w2, const float* s2,
+                     const void* base, int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t K, int64_t H,
+                     void* out, int64_t ld_out, void* scratch, int64_t scratch_bytes, void* stream) {
+  return run_moe_decode(fp8bs::Weights::kPlain, q, ldq, sf, ld_sf, topk_ids, weights, w13, s13, w2, s2, base, ld_base,
+                        T, topk, E, K, H, out, ld_out, scratch, scratch_bytes, stream);
+}
+
+int moe_decode_layer_preshuffled(const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf,
+                                 const int32_t* topk_ids, const float* weights, const void* w13, const float* s13,
+                                 const void* w2, const float* s2, const void* base, int64_t ld_base, int64_t T,
+                                 int32_t topk, int64_t E, int64_t K, int64_t H, void* out, int64_t ld_out,
+                                 void* scratch, int64_t scratch_bytes, void* stream) {
+  return run_moe_decode(fp8bs::Weights::kShuffled, q, ldq, sf, ld_sf, topk_ids, weights, w13, s13, w2, s2, base,
+                        ld_base, T, topk, E, K, H, out, ld_out, scratch, scratch_bytes, stream);
+}
+
+int moe_decode_layer_w4(const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf, const int32_t* topk_ids,
+                        const float* weights, const void* w13, const void* s13, const void* w2, const void* s2,
+                        const void* base, int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t K, int64_t H,
+                        void* out, int64_t ld_out, void* scratch, int64_t scratch_bytes, void* stream) {
+  return run_moe_decode(fp8bs::Weights::kW4, q, ldq, sf, ld_sf, topk_ids, weights, w13, s13, w2, s2, base, ld_base, T,
+                        topk, E, K, H, out, ld_out, scratch, scratch_bytes, stream);
+}
+
+int w4_group_quant(const void* w, int64_t rows, int64_t K, int32_t format, int32_t group, void* codes, void* scales,
+                   void* zeros, void* stream) {
+  int st = check_w4(rows, K, format, group, zeros);
+  if (st != FP8BS_OK) return st;
+  if (rows == 0) return FP8BS_OK;
+  if (!w || !codes || !scales) return FP8BS_ERR_NULL;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 2)) return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  hipError_t e = fp8bs::launch_w4_quant(static_cast<const uint16_t*>(w), rows, K, format == FP8BS_E2M1, group,
+                                        static_cast<uint8_t*>(codes), scales, static_cast<uint8_t*>(zeros),
+                                        static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int w4_preshuffle(const void* codes, const void* scales, const void* zeros, int64_t E, int64_t N, int64_t K,
+                  int32_t format, int32_t group, void* codes_out, void* scales_out, void* zeros_out, void* stream) {
+  if (E < 0 || N < 0 || N > (INT64_C(1) << 27) || E > (INT64_C(1) << 13)) return FP8BS_ERR_SHAPE;
+  int st = check_w4(E * N, K, format, group, zeros);
+  if (st != FP8BS_OK) return st;
+  if (E == 0 || N == 0) return FP8BS_OK;
+  if (!codes || !scales || !codes_out || !scales_out || !zeros != !zeros_out) return FP8BS_ERR_NULL;
+  if (!aligned(codes, 16) || !aligned(codes_out, 16) || !aligned(scales, 2) || !aligned(scales_out, 16) ||
+      !aligned_or_null(zeros_out, 16))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  hipError_t e = fp8bs::launch_w4_preshuffle(static_cast<const uint8_t*>(codes), scales,
+                                             static_cast<const uint8_t*>(zeros), E, N, K, format == FP8BS_E2M1, group,
+                                             static_cast<uint8_t*>(codes_out), scales_out,
+                                             static_cast<uint8_t*>(zeros_out), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FP8BS_OK : fail_hip(e);
+}
+
+int w4_group_gemv_nt(const void* x, int64_t ldx, const void* codes, const void* scales, const void* zeros, int64_t T,
+                     int64_t N, int64_t K, int32_t format, int32_t group, void* out, int64_t ld_out, void* stream) {
+  int st = check_w4(N, K, format, group, zeros);
+  if (st != FP8BS_OK) return st;
+  if (T < 0 || T > (INT64_C(1) << 21) || N > (INT64_C(1) << 27)) return FP8BS_ERR_SHAPE;
+  if (T == 0 || N == 0) return FP8BS_OK;
+  if (!x || !codes || !scales || !out) return FP8BS_ERR_NULL;
+  const int64_t most = INT64_C(1) << 31, rows = T < 64 ? T : 64;
+  if (ldx < K || ldx >= most || ((rows - 1) * ldx + K) * 2 >= most || ld_out < N) return FP8BS_ERR_SHAPE;
+  if (misaligned_rows(x, ldx) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned_or_null(zeros, 16) ||
+      !aligned(out, 2))
+    return FP8BS_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8BS_OK) return st;
+  fp8bs::W4Problem p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.ldx = ldx;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.codes = static_cast<const uint8_t*>(codes);
+  p.scales = scales;
+  p.zeros = static_cast<const uint8_t*>(zeros);
+  p.e2m1 = format == FP8BS_E2M1;
+  p.group = group;
+  p.out = static_cast<uint16_t*>(out);
+  p.ld_out = ld_out;
+  hipError_t e = fp8bs::launch_w4_gemv(p, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FP8BS_OK : fail_hip(e);
 }
 

@@ -458,6 +458,78 @@ int silu_mul_backward_from_checkpoint(const void* d_y, const int32_t* masked_m, 
                                       const void* cq, const uint32_t* csf, void* d_x, void* q, uint32_t* sf,
                                       void* stream);
 
+/*
+ * A mixture-of-experts layer for a few tokens (a decode step), from the router's choice to
+ * the layer's output, in two launches.  For token t and choice j with e = topk_ids[t][j] in
+ * [0, E), and v the values that codes stand for under their scales:
+ *   g, u   = v(q[t]) v(w13[e])^T            the first H rows of w13[e] and the last H, in fp32
+ *   y      = quantized(g / (1 + exp(-g)) * u)   1x128 groups, as fp8_quant_group_pack
+ *   out[t] = base[t] + sum_j weights[t][j] * (v(y) v(w2[e])^T)     fp32, bf16 at the end
+ * Pairs whose id is outside [0, E) are left out (a token without any gets base, or zeros); a
+ * token may name an expert twice.  It is what the dispatch quantization, the masked products,
+ * silu_mul_quant_group_pack and moe_combine compute, without their roundings of the products
+ * to bf16.  Values that are not finite stay with their token.
+ *   q        : e4m3 [T][ldq], 1 <= T <= 64;  sf : uint32 [ceil(K/512)][ld_sf], ld_sf >= T
+ *   topk_ids : int32 [T][topk];  weights : fp32 [T][topk];  1 <= topk <= 64
+ *   w13, s13 : e4m3 [E][2H][K], fp32 [E][2H/128][K/128];  w2, s2 : e4m3 [E][K][H], fp32
+ *              [E][K/128][H/128];  as the masked GEMMs take them.  1 <= E <= 1024
+ *   base     : bf16 [T][ld_base] or NULL;  out : bf16 [T][ld_out]
+ *   scratch  : moe_decode_layer_scratch_bytes(T, topk, H) bytes, 16-byte aligned, that no other
+ *              call uses until this one's work on the stream is done
+ *   K % 128 == 0 and H % 128 == 0, both at most 65536; the rows of q and of sf span less than 2 GiB.
+ * moe_decode_layer_preshuffled takes w13 and w2 in the layout of fp8_weight_preshuffle (rows = 2H
+ * and K of each expert), moe_decode_layer_w4 in e2m1 as w4_preshuffle lays them out.
+ * Equal calls give equal bits.
+ */
+int64_t moe_decode_layer_scratch_bytes(int64_t T, int32_t topk, int64_t H);
+int moe_decode_layer(const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf, const int32_t* topk_ids,
+                     const float* weights, const void* w13, const float* s13, const void* w2, const float* s2,
+                     const void* base, int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t K, int64_t H,
+                     void* out, int64_t ld_out, void* scratch, int64_t scratch_bytes, void* stream);
+int moe_decode_layer_preshuffled(const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf,
+                                 const int32_t* topk_ids, const float* weights, const void* w13, const float* s13,
+                                 const void* w2, const float* s2, const void* base, int64_t ld_base, int64_t T,
+                                 int32_t topk, int64_t E, int64_t K, int64_t H, void* out, int64_t ld_out,
+                                 void* scratch, int64_t scratch_bytes, void* stream);
+int moe_decode_layer_w4(const void* q, int64_t ldq, const uint32_t* sf, int64_t ld_sf, const int32_t* topk_ids,
+                        const float* weights, const void* w13, const void* s13, const void* w2, const void* s2,
+                        const void* base, int64_t ld_base, int64_t T, int32_t topk, int64_t E, int64_t K, int64_t H,
+                        void* out, int64_t ld_out, void* scratch, int64_t scratch_bytes, void* stream);
+
+/*
+ * Weights of 4 bits under group scales.  Two formats:
+ *   FP8BS_E2M1  codes of 1 + 2 + 1 bits (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), a UE8M0
+ *               byte b for every 32 columns: value = code * 2^(b - 127), b from 1 to 254
+ *   FP8BS_INT4  codes c = 0..15, a bf16 scale s for every 32, 64 or 128 columns, and a zero point z
+ *               (uint8) beside it, or 8 without one: value = s * (c - z)
+ * K % 128 == 0, K <= 65536.
+ *
+ * w4_group_quant: bf16 w [rows][K] (contiguous, finite) -> codes [rows][K/2] (even column in the low
+ *   half of a byte), scales [rows][K/group], zeros [rows][K/group] or NULL (FP8BS_INT4 only).
+ *     FP8BS_E2M1: the smallest 2^e with 6 * 2^e >= amax (e >= -126), codes to nearest even.
+ *     FP8BS_INT4: s = bf16(amax / 7), c = clamp(rint(w / s) + 8, 0, 15); with zeros s = bf16((max - min) / 15)
+ *     over the group's values and 0, z = min(rint(-min / s), 15), c = clamp(rint(w / s) + z, 0, 15), in
+ *     fp32; where s is 0, c = z (0 with zeros).
+ * w4_preshuffle: codes [E][N][K/2], scales and zeros [E][N][K/group] in row order -> the layout that the
+ *   products read, rows past N and columns past K zero, with tiles = ceil(N/16), units = ceil(K/512):
+ *     codes_out  [E][tiles][K/128][64][16 bytes]   entry 16 c + r of a tile is row r:
+ *       FP8BS_E2M1  columns 32 c .. 32 c + 31;  FP8BS_INT4  in 32-bit word i the columns 32 i + 8 c +
+ *       0, 2, 4, 6, 1, 3, 5, 7, from the low bits up
+ *     scales_out, zeros_out   FP8BS_E2M1  [E][tiles][units][64][4]: byte b of entry 16 c + r is group
+ *       4 b + c of row r;  FP8BS_INT4  [E][tiles][units][16][512/group]
+ * w4_group_gemv_nt: out[t][n] = bf16( sum over k of x[t][k] * w[n][k] ), w in that layout (E = 1), sums in
+ *   fp32.  Made for few rows of x: every 64 of them read the weights once.  zeros may be NULL.
+ *   x : bf16 [T][ldx];  out : bf16 [T][ld_out], ld_out >= N, rows 2-byte aligned;  T <= 2^21, N <= 2^27,
+ *   64 rows of x span less than 2 GiB.
+ */
+enum { FP8BS_E2M1 = 0, FP8BS_INT4 = 1 };
+int w4_group_quant(const void* w, int64_t rows, int64_t K, int32_t format, int32_t group, void* codes, void* scales,
+                   void* zeros, void* stream);
+int w4_preshuffle(const void* codes, const void* scales, const void* zeros, int64_t E, int64_t N, int64_t K,
+                  int32_t format, int32_t group, void* codes_out, void* scales_out, void* zeros_out, void* stream);
+int w4_group_gemv_nt(const void* x, int64_t ldx, const void* codes, const void* scales, const void* zeros, int64_t T,
+                     int64_t N, int64_t K, int32_t format, int32_t group, void* out, int64_t ld_out, void* stream);
+
 /* Status helpers. */
 const char* fp8bs_status_string(int status);
 int fp8bs_last_hip_error(void);
