@@ -18,6 +18,110 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every run: the load gives zeros
 
+// A K-block of one tile as a lane holds it.  GP: groups in its 128 columns of integers (0: e2m1).
+template <int GP, bool Z>
+struct Block {
+  static constexpr bool E2M1 = GP == 0;
+  u32x4 w;
+  uint32_t s[GP == 4 ? 2 : 1], z;
+
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rz, int q,
+                                       int j, uint32_t past, int KB, uint32_t s_tile, uint32_t z_tile, int lane) {
+    const uint32_t u = (uint32_t)j >> 2, k = (uint32_t)j & 3, r = lane & 15;
+    w = run_load16(rw, (uint32_t)((q * KB + j) * 1024 + 16 * lane) | past);
+    if constexpr (E2M1) {
+      s[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)((q * s_tile + u * 256 + 4 * lane + k) | past), 0, 0);
+    } else {
+      const uint32_t o = (q * s_tile + (u * 16 + r) * 8 * GP + k * 2 * GP) | past;
+      if constexpr (GP == 1) s[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)o, 0, 0);
+      if constexpr (GP == 2) s[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, (int)o, 0, 0);
+      if constexpr (GP == 4) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)o, 0, 0));
+        s[0] = v[0];
+        s[1] = v[1];
+      }
+      if constexpr (Z) {
+        const uint32_t oz = (q * z_tile + (u * 16 + r) * 4 * GP + k * GP) | past;
+        if constexpr (GP == 1) z = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rz, (int)oz, 0, 0);
+        if constexpr (GP == 2) z = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rz, (int)oz, 0, 0);
+        if constexpr (GP == 4) z = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rz, (int)oz, 0, 0);
+      }
+    }
+  }
+  // The codes as bf16: e2m1 with their scale, integers as 16 + c.
+  __device__ __forceinline__ void decode(bf16x8 (&v)[4]) const {
+    if constexpr (E2M1) {
+      const uint32_t byte = s[0] & 0xFF;
+      const float scale = __uint_as_float(byte ? byte << 23 : 0x400000u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], scale, 0);
+        const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], scale, 1);
+        const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], scale, 2);
+        const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], scale, 3);
+        v[k] = bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+      }
+    } else {
+      // mantissa bits of a code, and 16 in bf16, twice; in registers, so that both take one instruction
+      uint32_t mask = 0x00780078u, base = 0x41804180u;
+      asm("" : "+s"(mask), "+v"(base));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t d = w[k];
+        const u32x4 o = {((d << 3) & mask) | base, ((d >> 1) & mask) | base, ((d >> 5) & mask) | base,
+                         ((d >> 9) & mask) | base};
+        v[k] = __builtin_bit_cast(bf16x8, o);
+      }
+    }
+  }
+  __device__ __forceinline__ float scale(int g) const { return g & 1 ? bf16_hi(s[g / 2]) : bf16_lo(s[g / 2]); }
+  __device__ __forceinline__ float zero(int g) const { return (float)((z >> (8 * g)) & 0xFF); }
+};
+
+__device__ __forceinline__ bf16x8 eight_of(float v) {
+  const __bf16 b = (__bf16)v;
+  return bf16x8{b, b, b, b, b, b, b, b};
+}
+
+// acc[q] += x (16 tokens) times a K-block of RT tiles.  x: the lane's four operands.
+template <int GP, bool Z, int RT>
+__device__ __forceinline__ void multiply(v4f (&acc)[RT], const bf16x8 (&x)[4], const Block<GP, Z> (&w)[RT],
+                                         const bf16x8 (&v)[RT][4]) {
+  if constexpr (GP == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int q = 0; q < RT; ++q) acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[k], v[q][k], acc[q], 0, 0, 0);
+  } else {
+    constexpr int N = GP == 0 ? 4 : 4 / GP;  // operands a group
+    // what the codes' values have too much: with zero points 16, without them 24
+    const bf16x8 much = eight_of(Z ? -16.0f : -24.0f), ones = eight_of(1.0f);
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      v4f o = {0, 0, 0, 0}, sx = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = g * N; k < (g + 1) * N; ++k) {  // the same for every tile
+        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[k], much, o, 0, 0, 0);
+        if constexpr (Z) sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[k], ones, sx, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        v4f d = o;
+#pragma unroll
+        for (int k = g * N; k < (g + 1) * N; ++k) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[k], v[q][k], d, 0, 0, 0);
+        const float s = w[q].scale(g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[q][i] = __builtin_fmaf(s, Z ? __builtin_fmaf(-w[q].zero(g), sx[i], d[i]) : d[i], acc[q][i]);
+      }
+    }
+  }
+  // the sums are brought up to here before anything after it: left to itself the compiler puts them off and
+  // keeps what they are of in registers
+#pragma unroll
+  for (int q = 0; q < RT; ++q) asm volatile("" : "+v"(acc[q]));
+}
+
 // ------------------------------------------------------------------ product
 
 // out[t][n] = sum over k of x[t][k] w[n][k] for 16 rows n of w and up to 16 CB tokens t.
@@ -28,141 +132,211 @@ constexpr uint32_t kOut = 0x80000000u;  // an offset past every run: the load gi
 //
 // e2m1 codes become bf16 with their scale by one conversion for two (exact: a power of two).
 // Integer codes c become 16 + c by putting them into the mantissa of a bf16, a shift and a
-// mask for two; with S = sum of x over the group (a product with ones, in the same lanes),
-//   sum x s (c - z) = s (sum x (16 + c) - (16 + z) S).
-// 16 is the smallest offset that takes all sixteen codes; the subtraction costs the fp32 sum
-// at most (16 + 15 + 16 + 15) / 1 of its relative error in the largest term, far under the
-// bf16 rounding of the result.
-template <int GP, bool Z, int CB>
-__global__ __launch_bounds__(256) void w4_gemv_kernel(const W4Problem p) {
+// mask for two, and a second product takes 16 + z times the sum of x off again:
+//   sum x s (c - z) = s (sum x (16 + c) - sum x (16 + z)).
+// 16 is the smallest offset that takes all sixteen codes: the fp32 sum's error grows by the ratio
+// of 16 + c to |c - z|, far under the bf16 rounding of the result.
+template <int GP, bool Z, int SL, int CB, int RT, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) {
   constexpr bool E2M1 = GP == 0;
-  constexpr int NS = E2M1 ? 1 : 2 * GP, NZ = Z ? GP : 1;  // words of scales and zero points a lane and unit
-  __shared__ __attribute__((aligned(16))) float part[4][CB][64][4];
+  constexpr int D = CB <= 2 ? 4 : 2;  // K-blocks ahead
+  constexpr int TS = 16 / SL;         // tokens a slot
+  __shared__ __attribute__((aligned(16))) float part[NW][CB * RT][64][4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane >> 4, r = lane & 15;
-  const int64_t tile = blockIdx.x, t0 = (int64_t)blockIdx.y * 64;
-  const int T = (int)(p.T - t0 < 16 * CB ? p.T - t0 : 16 * CB);
+  const int64_t tile = (int64_t)blockIdx.x * RT, t0 = (int64_t)blockIdx.y * 64;
+  const int tiles = (int)((p.N + 15) / 16 - tile < RT ? (p.N + 15) / 16 - tile : RT);
+  const int T = (int)(p.T - t0 < TS * CB ? p.T - t0 : TS * CB);
   const int KB = (int)(p.K / 128), units = (KB + 3) / 4;
-  const auto rw = shared_run(p.codes + tile * KB * 1024, KB * 1024u);
+  const uint32_t s_tile = units * (E2M1 ? 256u : 128u * GP), z_tile = units * 64u * GP;
+  const auto rw = shared_run(p.codes + tile * KB * 1024, tiles * KB * 1024u);
   const auto rx = shared_run(p.x + t0 * p.ldx, (uint32_t)(((T - 1) * p.ldx + p.K) * 2));
-  const auto rs = shared_run(static_cast<const uint8_t*>(p.scales) + tile * units * (E2M1 ? 256 : 128 * GP),
-                             units * (E2M1 ? 256u : 128u * GP));
-  const auto rz = shared_run(Z ? p.zeros + tile * units * (64 * GP) : p.codes, Z ? units * 64u * GP : 0u);
+  const auto rs = shared_run(static_cast<const uint8_t*>(p.scales) + tile * s_tile, tiles * s_tile);
+  const auto rz = shared_run(Z ? p.zeros + tile * z_tile : p.codes, Z ? tiles * z_tile : 0u);
   uint32_t x_at[CB];
 #pragma unroll
   for (int b = 0; b < CB; ++b)
-    x_at[b] = 16 * b + r < T ? (uint32_t)((16 * b + r) * p.ldx * 2) + (E2M1 ? 64 * c : 16 * c) : kOut;
+    x_at[b] = 16 * b + r % TS < T ? (uint32_t)((16 * b + r % TS) * p.ldx * 2) + (E2M1 ? 64 * c : 16 * c) + 256 * (r / TS)
+                                 : kOut;
 
-  const int u0 = units * wave / 4, u1 = units * (wave + 1) / 4;
-  u32x4 w[4];
-  uint32_t s[NS], z[NZ], s_next[NS], z_next[NZ];
-  v4f acc[CB];
+  const int j0 = KB * wave / NW, j1 = KB * (wave + 1) / NW;
+  Block<GP, Z> w[D][RT];
+  bf16x8 x[D / SL][CB][4], x_ahead[CB][4];
+  v4f acc[CB][SL][RT];
 #pragma unroll
-  for (int b = 0; b < CB; ++b) acc[b] = v4f{0, 0, 0, 0};
-  auto load_w = [&](int j, int i) { w[i] = run_load16(rw, j < KB ? (uint32_t)(j * 1024 + 16 * lane) : kOut); };
-  auto load_s = [&](int u) {
-    const uint32_t past = u < units ? 0 : kOut;
-    if constexpr (E2M1) {
-      s_next[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, (int)((uint32_t)(u * 256 + 4 * lane) | past), 0, 0);
-    } else {
-      const uint32_t o = (uint32_t)((u * 16 + r) * 8 * GP) | past;
+  for (int b = 0; b < CB; ++b)
 #pragma unroll
-      for (int i = 0; i < NS; i += 2) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(o + 4 * i), 0, 0));
-        s_next[i] = v[0];
-        s_next[i + 1] = v[1];
-      }
-      if constexpr (Z) {
+    for (int i = 0; i < SL * RT; ++i) acc[b][i / RT][i % RT] = v4f{0, 0, 0, 0};
+  auto load_w = [&](int j, int i) {
 #pragma unroll
-        for (int i = 0; i < NZ; ++i)
-          z_next[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rz, (int)((uint32_t)((u * 16 + r) * 4 * GP + 4 * i) | past), 0, 0);
-      }
-    }
+    for (int q = 0; q < RT; ++q) w[i][q].load(rw, rs, rz, q, j, j < j1 ? 0 : kOut, KB, s_tile, z_tile, lane);
   };
-  if (u0 < u1) {
-    load_s(u0);
+  // tokens of the SL K-blocks from j; a slot past the range has zeros (what lies there is the next token's, and a value
+  // of it that is not finite would not vanish against weights of zero)
+  auto load_x = [&](int j, bf16x8(&to)[CB][4]) {
+    const uint32_t past = j + r / TS < j1 ? 0 : kOut;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_w(4 * u0 + i, i);
+    for (int b = 0; b < CB; ++b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        to[b][k] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                                                    rx, (int)((x_at[b] + (uint32_t)(256 * j + (E2M1 ? 16 : 64) * k)) | past), 0, 0));
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    load_w(j0 + i, i);
+    if (i % SL == 0) load_x(j0 + i, x[i / SL]);
+    __builtin_amdgcn_sched_barrier(0);  // in the loop's order, or its waits are for all of them
   }
-  for (int u = u0; u < u1; ++u) {
+  auto step = [&](int j, auto i_tag) {
+    constexpr int I = decltype(i_tag)::value, IX = I / SL, S = I % SL;
+    if constexpr (SL == D && S == 0) load_x(j + D, x_ahead);
+    bf16x8 v[RT][4];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) s[i] = s_next[i];
+    for (int q = 0; q < RT; ++q) w[I][q].decode(v[q]);
 #pragma unroll
-    for (int i = 0; i < NZ; ++i) z[i] = Z ? z_next[i] : 0;
-    load_s(u + 1 < u1 ? u + 1 : units);
+    for (int b = 0; b < CB; ++b) multiply<GP, Z, RT>(acc[b][S], x[IX][b], w[I], v);
+    load_w(j + D, I);
+    if constexpr (SL < D && S == SL - 1) load_x(j - S + D, x[IX]);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay here: D K-blocks ahead of their products
+  };
+  for (int j = j0; j < j1; j += D) {
+    // K-blocks past the range have weights and tokens of zeros
+    step(j, std::integral_constant<int, 0>{});
+    step(j + 1, std::integral_constant<int, 1>{});
+    if constexpr (D == 4) {
+      step(j + 2, std::integral_constant<int, 2>{});
+      step(j + 3, std::integral_constant<int, 3>{});
+    }
+    if constexpr (SL == D) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = 4 * u + i;
-      bf16x8 x[CB][4];
-#pragma unroll
-      for (int b = 0; b < CB; ++b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          x[b][k] = __builtin_bit_cast(
-              bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
-                          rx, (int)(j < KB ? x_at[b] + (uint32_t)(256 * j + (E2M1 ? 16 : 64) * k) : kOut), 0, 0));
-      bf16x8 v[4];
-      if constexpr (E2M1) {
-        const uint32_t byte = (s[0] >> (8 * i)) & 0xFF;
-        const float scale = __uint_as_float(byte ? byte << 23 : 0x400000u);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i][k], scale, 0);
-          const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i][k], scale, 1);
-          const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i][k], scale, 2);
-          const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i][k], scale, 3);
-          v[k] = bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t d = w[i][k];
-          const u32x4 o = {((d << 3) & 0x00780078u) | 0x41804180u, ((d >> 1) & 0x00780078u) | 0x41804180u,
-                           ((d >> 5) & 0x00780078u) | 0x41804180u, ((d >> 9) & 0x00780078u) | 0x41804180u};
-          v[k] = __builtin_bit_cast(bf16x8, o);
-        }
-      }
-      load_w(j + 4 < 4 * u1 ? j + 4 : KB, i);
-      if constexpr (E2M1) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int b = 0; b < CB; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[b][k], v[k], acc[b], 0, 0, 0);
-      } else {
-        const __bf16 one = (__bf16)1.0f;
-        const bf16x8 ones = {one, one, one, one, one, one, one, one};
-#pragma unroll
-        for (int gr = 0; gr < GP; ++gr) {
-          const int at = i * GP + gr;
-          const float scale = at & 1 ? bf16_hi(s[at / 2]) : bf16_lo(s[at / 2]);
-          const float off = Z ? 16.0f + (float)((z[at / 4] >> (8 * (at % 4))) & 0xFF) : 24.0f;
-#pragma unroll
-          for (int b = 0; b < CB; ++b) {
-            v4f d = {0, 0, 0, 0}, sx = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = gr * (4 / GP); k < (gr + 1) * (4 / GP); ++k) {
-              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[b][k], v[k], d, 0, 0, 0);
-              sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[b][k], ones, sx, 0, 0, 0);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[b][q] = __builtin_fmaf(scale, __builtin_fmaf(-off, sx[q], d[q]), acc[b][q]);
-          }
-        }
-      }
+      for (int k = 0; k < 4; ++k) x[0][0][k] = x_ahead[0][k];
     }
   }
+  // of the rows 4 c + i, slot s has its own: those of c / (4 / SL) == s
 #pragma unroll
-  for (int b = 0; b < CB; ++b) *reinterpret_cast<v4f*>(part[wave][b][lane]) = acc[b];
+  for (int b = 0; b < CB; ++b)
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      v4f v = acc[b][0][q];
+#pragma unroll
+      for (int i = 1; i < SL; ++i)
+        if (c / (4 / SL) == i) v = acc[b][i][q];
+      *reinterpret_cast<v4f*>(part[wave][b * RT + q][lane]) = v;
+    }
   __syncthreads();
-  for (int i = threadIdx.x; i < CB * 256; i += 256) {
-    const int n = i & 15, t = i >> 4;  // of lane 16 (t % 16 / 4) + n, register t % 4
+  for (int i = threadIdx.x; i < CB * RT * 16 * TS; i += NW * 64) {
+    // row n of tile q and token t: register t % 4 of lanes 16 c + n, c = t % 16 / 4 and the same of the other slots
+    const int n = i % (16 * RT), q = n >> 4, t = i / (16 * RT);
     if (t < T && tile * 16 + n < p.N) {
-      const int l = 16 * ((t & 15) >> 2) + n, b = t >> 4, q = t & 3;
-      const float v = (part[0][b][l][q] + part[1][b][l][q]) + (part[2][b][l][q] + part[3][b][l][q]);
+      const int l = 16 * ((t & 15) >> 2) + (n & 15), at = (t >> 4) * RT + q;
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k)
+#pragma unroll
+        for (int s2 = 0; s2 < SL; ++s2) v += part[k][at][l + 64 / SL * s2][t & 3];
       p.out[(t0 + t) * p.ld_out + tile * 16 + n] = (uint16_t)(bf16x2_rne(v, v) & 0xFFFF);
     }
   }
+}
+
+// The same for up to 16 CB tokens that four wavefronts of different rows share through LDS, 64 RT rows a
+// workgroup: the tokens are read from the L2 once for all of them, KC K-blocks at a time, each chunk while
+// the one before it is worked on.  (16 x 18432 x 7168 in e2m1: 18.5 us; w4_gemv_kernel, whose wavefronts
+// each read all tokens: 33.)
+template <int GP, bool Z, int CB, int RT>
+__global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
+  constexpr bool E2M1 = GP == 0;
+  constexpr int KC = CB <= 2 ? 4 : 2;  // K-blocks a chunk of tokens
+  constexpr int PIECES = CB * KC;      // pieces of eight values that a thread brings
+  constexpr int XB = KC * 16 * CB * 256;
+  __shared__ __attribute__((aligned(16))) uint8_t xl[2][XB];  // [block][token][16 pieces, piece k at k ^ token % 16]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane >> 4, r = lane & 15;
+  const int all_tiles = (int)((p.N + 15) / 16);
+  const int tile = ((int)blockIdx.x * 4 + wave) * RT;
+  const int64_t t0 = (int64_t)blockIdx.y * 64;
+  const int T = (int)(p.T - t0 < 16 * CB ? p.T - t0 : 16 * CB);
+  const int tiles = all_tiles - tile < 0 ? 0 : all_tiles - tile < RT ? all_tiles - tile : RT;
+  const int KB = (int)(p.K / 128), units = (KB + 3) / 4;
+  const uint32_t s_tile = units * (E2M1 ? 256u : 128u * GP), z_tile = units * 64u * GP;
+  const auto rw = shared_run(p.codes + (int64_t)tile * KB * 1024, tiles * KB * 1024u);
+  const auto rx = shared_run(p.x + t0 * p.ldx, (uint32_t)(((T - 1) * p.ldx + p.K) * 2));
+  const auto rs = shared_run(static_cast<const uint8_t*>(p.scales) + tile * (int64_t)s_tile, tiles * s_tile);
+  const auto rz = shared_run(Z ? p.zeros + tile * (int64_t)z_tile : p.codes, Z ? tiles * z_tile : 0u);
+  Block<GP, Z> w[KC][RT];
+  u32x4 xn[PIECES];
+  v4f acc[CB][RT];
+#pragma unroll
+  for (int b = 0; b < CB; ++b)
+#pragma unroll
+    for (int q = 0; q < RT; ++q) acc[b][q] = v4f{0, 0, 0, 0};
+  auto load_w = [&](int j, int i) {
+#pragma unroll
+    for (int q = 0; q < RT; ++q) w[i][q].load(rw, rs, rz, q, j, j < KB ? 0 : kOut, KB, s_tile, z_tile, lane);
+  };
+  // pieces of a chunk: thread -> (token, K-block, piece), the pieces of a token's chunk side by side
+  auto load_x = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int at = i * 256 + tid, t = at / (16 * KC), k = at % (16 * KC);
+      const uint32_t o = t < T && j + k / 16 < KB ? (uint32_t)(t * p.ldx * 2 + j * 256 + k * 16) : kOut;
+      xn[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)o, 0, 0));
+    }
+  };
+  auto store_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int at = i * 256 + tid, t = at / (16 * KC), k = at % (16 * KC), kb = k / 16, piece = k & 15;
+      *reinterpret_cast<u32x4*>(&xl[buf][((kb * 16 * CB + t) * 16 + (piece ^ (t & 15))) * 16]) = xn[i];
+    }
+  };
+  load_x(0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < KC; ++i) {
+    load_w(i, i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  store_x(0);
+  __syncthreads();
+  auto chunk = [&](int j, int buf) {
+    load_x(j + KC);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      bf16x8 v[RT][4];
+#pragma unroll
+      for (int q = 0; q < RT; ++q) w[i][q].decode(v[q]);
+#pragma unroll
+      for (int b = 0; b < CB; ++b) {
+        bf16x8 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = *reinterpret_cast<const bf16x8*>(
+              &xl[buf][((i * 16 * CB + 16 * b + r) * 16 + ((E2M1 ? 4 * c + k : 4 * k + c) ^ r)) * 16]);
+        multiply<GP, Z, RT>(acc[b], x, w[i], v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      load_w(j + KC + i, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    store_x(buf ^ 1);
+    __syncthreads();
+  };
+  for (int j = 0, buf = 0; j < KB; j += KC, buf ^= 1) chunk(j, buf);
+#pragma unroll
+  for (int b = 0; b < CB; ++b)
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * b + 4 * c + i;
+        const int64_t n = (int64_t)(tile + q) * 16 + r;
+        if (t < T && n < p.N) p.out[(t0 + t) * p.ld_out + n] = (uint16_t)(bf16x2_rne(acc[b][q][i], 0.0f) & 0xFFFF);
+      }
 }
 
 // ------------------------------------------------------------------ weights
@@ -261,17 +435,39 @@ __global__ __launch_bounds__(256) void w4_scales_kernel(const V* __restrict__ sc
   }
 }
 
+template <int GP, bool Z, int RT>
+hipError_t launch_rows(const W4Problem& p, int most, dim3 grid, hipStream_t stream) {
+  constexpr int NW = 4;
+  if (most <= 4) w4_gemv_kernel<GP, Z, 4, 1, RT, NW><<<grid, NW * 64, 0, stream>>>(p);
+  else if (most <= 8) w4_gemv_kernel<GP, Z, 2, 1, RT, NW><<<grid, NW * 64, 0, stream>>>(p);
+  else if (most <= 16) w4_gemv_kernel<GP, Z, 1, 1, RT, NW><<<grid, NW * 64, 0, stream>>>(p);
+  else if (most <= 32) w4_gemv_kernel<GP, Z, 1, 2, RT, NW><<<grid, NW * 64, 0, stream>>>(p);
+  else if (most <= 48) w4_gemv_kernel<GP, Z, 1, 3, RT, NW><<<grid, NW * 64, 0, stream>>>(p);
+  else w4_gemv_kernel<GP, Z, 1, 4, RT, NW><<<grid, NW * 64, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// Which kernel.  Up to one tile a compute unit (256), each is a workgroup's, so that all of them work; with more,
+// a wavefront takes two and reads its tokens once for both (1 x 7168 x 18432: 13.2 us against 14.4, 64 x 7168 x
+// 2048: 12.7 against 19.5; at 256 tiles 1 x 4096 x 7168: 7.0 against 5.9).  From 1024 tiles and 5 tokens the rows
+// alone fill the chip with wavefronts that share the tokens through LDS.
 template <int GP, bool Z>
 hipError_t launch_gemv(const W4Problem& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)((p.T + 63) / 64));
-  const int64_t most = p.T < 64 ? p.T : 64;
-  switch ((most + 15) / 16) {
-    case 1: w4_gemv_kernel<GP, Z, 1><<<grid, 256, 0, stream>>>(p); break;
-    case 2: w4_gemv_kernel<GP, Z, 2><<<grid, 256, 0, stream>>>(p); break;
-    case 3: w4_gemv_kernel<GP, Z, 3><<<grid, 256, 0, stream>>>(p); break;
-    default: w4_gemv_kernel<GP, Z, 4><<<grid, 256, 0, stream>>>(p); break;
+  const int64_t tiles = (p.N + 15) / 16;
+  const int most = (int)(p.T < 64 ? p.T : 64);
+  const unsigned chunks = (unsigned)((p.T + 63) / 64);
+  if (most > 4 && tiles >= 1024) {
+    const dim3 grid((unsigned)((tiles + 7) / 8), chunks);
+    switch ((most + 15) / 16) {
+      case 1: w4_batch_kernel<GP, Z, 1, 2><<<grid, 256, 0, stream>>>(p); break;
+      case 2: w4_batch_kernel<GP, Z, 2, 2><<<grid, 256, 0, stream>>>(p); break;
+      case 3: w4_batch_kernel<GP, Z, 3, 2><<<grid, 256, 0, stream>>>(p); break;
+      default: w4_batch_kernel<GP, Z, 4, 2><<<grid, 256, 0, stream>>>(p); break;
+    }
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  return tiles <= 256 ? launch_rows<GP, Z, 1>(p, most, dim3((unsigned)tiles, chunks), stream)
+                      : launch_rows<GP, Z, 2>(p, most, dim3((unsigned)((tiles + 1) / 2), chunks), stream);
 }
 
 unsigned blocks_of(int64_t threads) {
