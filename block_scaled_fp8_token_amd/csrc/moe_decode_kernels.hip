@@ -19,6 +19,8 @@
 // Lane l = 16 c + r holds of a 128-wide K-block of row (or token) r: of e4m3 the columns
 // 16 c .. 16 c + 15 and 64 + 16 c .. + 15, of e2m1 the columns 32 c .. 32 c + 31, eight of
 // them a product; the result holds rows 4 c + i, i < 4, of token r.
+#include <type_traits>
+
 #include "block_device.hpp"
 #include "decode_launch.hpp"
 
@@ -32,7 +34,19 @@ struct MoeArgs {
   MoeDecodeProblem m;
   uint8_t* y;       // e4m3 [T * topk][H]
   uint32_t* y_sf;   // [T * topk][ceil(H / 512)], the bytes of four groups to a word
+  float* y32;       // or y in fp32 [T * topk][H], where few experts are chosen
 };
+
+// Bytes of a row of y quantized in LDS: whole units of 512, and 16 more that keep the rows of a product's tokens apart in
+// the banks.
+__host__ __device__ constexpr int row_bytes(int H) { return (H + 511) / 512 * 512 + 16; }
+
+// Few experts: workgroups of 128 columns of y would not be one a compute unit, and y is small enough for every workgroup of
+// the second kernel to quantize all of it.
+bool splits(const MoeDecodeProblem& m) {
+  const int pairs = m.T * m.topk, experts = m.E < pairs ? m.E : pairs;
+  return pairs <= 64 && m.T <= 16 && experts * (m.H / 128) < 256 && pairs * row_bytes(m.H) <= 36864;
+}
 
 __device__ __forceinline__ u32x4 cached16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
@@ -46,11 +60,16 @@ template <Weights F>
 struct Unit {
   static constexpr int L = F == Weights::kW4 ? 1 : 2;
   u32x4 w[4][L];
-  uint32_t s[F == Weights::kW4 ? 1 : 4];
-  uint32_t s_ahead;  // 4-bit weights: the next unit's word of scales
+  using Scales = std::conditional_t<F == Weights::kW4, uint32_t, u32x4>;
+  Scales s, s_ahead;  // of this unit and the next
 
-  __device__ __forceinline__ void begin() {
-    if constexpr (F == Weights::kW4) s[0] = s_ahead;
+  // Scales of the unit from K-block j, of KB in all (those past the end are zeros).
+  __device__ __forceinline__ void begin(int j, int KB) {
+    s = s_ahead;
+    if constexpr (F != Weights::kW4) {
+#pragma unroll
+      for (int i = 1; i < 4; ++i) s[i] = j + i < KB ? s[i] : 0;
+    }
   }
 };
 
@@ -83,9 +102,9 @@ struct Rows {
       s = shared_run(static_cast<const float*>(scales) + (e * (N / 128) + n0 / 128) * KB, KB * 4u);
     }
   }
-  // K-block j = 4 u + i
-  __device__ __forceinline__ void load(Unit<F>& v, int j, int i) const {
-    const uint32_t past = j < KB ? 0 : kOut;
+  // K-block j = 4 u + i (nothing from `end` on)
+  __device__ __forceinline__ void load(Unit<F>& v, int j, int i, int end) const {
+    const uint32_t past = j < end ? 0 : kOut;
     if constexpr (F == Weights::kW4) {
       v.w[i][0] = run_load16(w, (at + j * 1024) | past);
       if (i == 0) v.s_ahead = cached4(s, (uint32_t)(j * 64 + at / 4) | past);
@@ -93,7 +112,7 @@ struct Rows {
       const uint32_t o = at + j * (F == Weights::kShuffled ? 4096 : 128);
       v.w[i][0] = run_load16(w, o | past);
       v.w[i][1] = run_load16(w, (o + (F == Weights::kShuffled ? 2048 : 64)) | past);
-      v.s[i] = cached4(s, (uint32_t)(j * 4) | past);
+      if (i == 0) v.s_ahead = cached16(s, (uint32_t)(j * 4) | past);
     }
   }
 };
@@ -113,7 +132,7 @@ __device__ __forceinline__ float scale_of(uint32_t word, int i) { return __uint_
 template <Weights F, int I>
 __device__ __forceinline__ bf16x8 rows_of(const Unit<F>& v, int m) {
   if constexpr (F == Weights::kW4) {
-    const float scale = scale_of(v.s[0], I);
+    const float scale = scale_of(v.s, I);
     const uint32_t w = v.w[I][0][m];
     const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
     const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
@@ -137,88 +156,194 @@ constexpr int kFirst = F == Weights::kW4 ? 32 : 16;
 template <Weights F>
 constexpr int kSecond = F == Weights::kW4 ? 16 : 64;
 
+// The sums are brought up to here before anything after it: left to itself the compiler puts them off and keeps what
+// they are of in registers.
+template <int N>
+__device__ __forceinline__ void pin(v4f (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
 // The bytes of a scale word that belong to K-blocks past the end are cleared.
 __device__ __forceinline__ uint32_t valid_bytes(uint32_t word, int blocks_left) {
   return blocks_left >= 4 ? word : blocks_left <= 0 ? 0 : word & ((1u << (8 * blocks_left)) - 1);
 }
 
-// The experts that some token has chosen, as bits; ids [T][topk] to LDS.  Every thread calls it.
-__device__ __forceinline__ void chosen(const MoeDecodeProblem& m, int* ids, uint32_t* bits) {
-  const int pairs = m.T * m.topk;
-  if (threadIdx.x < 32) bits[threadIdx.x] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int e = m.ids[i];
-    ids[i] = e;
-    if (e >= 0 && e < m.E) atomicOr(&bits[e >> 5], 1u << (e & 31));
+// ------------------------------------------------------------------ routing
+
+// The tokens of one expert as columns of the products, an entry each, in the tokens' order.
+struct Columns {
+  int token[64], pair[64];
+  float weight[64];
+};
+
+// What a workgroup knows of the routing.  Up to 64 pairs (SMALL) lie one a lane and each wavefront finds its way among them
+// by itself; more go to LDS, ids and weights [choice][token], with the list of the experts that some token has
+// chosen.  Experts come in the order of the first pair that names them (SMALL) or in their own.
+template <bool SMALL>
+struct Routing {
+  // SMALL: this lane's pair
+  int id = -1;
+  float weight = 0.0f;   // of the token's pairs of this expert together
+  bool column = false;   // the first of them
+  uint64_t firsts = 0;   // lanes whose expert no earlier pair has
+  // else
+  const int* ids = nullptr;
+  const float* weights = nullptr;
+  const uint16_t* list = nullptr;
+  int T = 0, topk = 0, active = 0;
+
+  static constexpr int words(int topk) { return SMALL ? 0 : 2 * 64 * topk + kMoeDecodeMaxE / 2 + 32; }
+
+  // Every thread of the workgroup; lds: words(topk) words (none if SMALL).
+  __device__ __forceinline__ void open(const MoeDecodeProblem& m, int lane, uint32_t* lds, bool with_weights) {
+    T = m.T;
+    topk = m.topk;
+    const int pairs = m.T * m.topk;
+    if constexpr (SMALL) {
+      const bool has = lane < pairs;
+      int e = has ? m.ids[lane] : -1;
+      const float w = has && with_weights ? m.weights[lane] : 0.0f;
+      id = e >= 0 && e < m.E ? e : -1;
+      const int t = lane / topk;
+      bool first = true;
+      column = id >= 0;
+      for (int p = 0; p < pairs; ++p) {
+        const int other = __builtin_amdgcn_readlane(id, p);
+        const bool same = other == id, mine = same && p / topk == t;
+        if (mine) weight += read_lane(w, p);
+        first &= !(same && p < lane);
+        column &= !(mine && p < lane);
+      }
+      firsts = __ballot(id >= 0 && first);
+      active = __builtin_popcountll(firsts);
+    } else {
+      int* to_ids = reinterpret_cast<int*>(lds);
+      float* to_weights = reinterpret_cast<float*>(lds + 64 * topk);
+      uint16_t* to_list = reinterpret_cast<uint16_t*>(lds + 128 * topk);
+      uint32_t* bits = lds + 128 * topk + kMoeDecodeMaxE / 2;
+      if (threadIdx.x < 32) bits[threadIdx.x] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+        const int at = i % topk * 64 + i / topk, e = m.ids[i];
+        to_ids[at] = e;
+        if (with_weights) to_weights[at] = m.weights[i];
+        if (e >= 0 && e < m.E) atomicOr(&bits[e >> 5], 1u << (e & 31));
+      }
+      __syncthreads();
+      const int n = (m.E + 31) / 32;
+      for (int i = threadIdx.x; i < m.E; i += blockDim.x) {
+        if (bits[i >> 5] >> (i & 31) & 1) {
+          int rank = __builtin_popcount(bits[i >> 5] & ((1u << (i & 31)) - 1));
+          for (int k = 0; k < (i >> 5); ++k) rank += __builtin_popcount(bits[k]);
+          to_list[rank] = (uint16_t)i;
+        }
+      }
+      for (int k = 0; k < n; ++k) active += __builtin_popcount(bits[k]);
+      active = __builtin_amdgcn_readfirstlane(active);
+      __syncthreads();
+      ids = to_ids;
+      weights = to_weights;
+      list = to_list;
+    }
   }
-  __syncthreads();
-}
+  // The a-th of the active experts.
+  __device__ __forceinline__ int expert(int a, int lane) const {
+    if constexpr (SMALL) {
+      const int rank = __builtin_popcountll(firsts & ((1ull << lane) - 1));
+      return __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(__ballot((firsts >> lane & 1) && rank == a)));
+    } else {
+      return __builtin_amdgcn_readfirstlane(list[a]);
+    }
+  }
+  // Its columns, written by the calling wavefront; how many.
+  __device__ __forceinline__ int columns(int e, int lane, Columns& to) const {
+    int pair = -1, t = lane;
+    float w = 0.0f;
+    if constexpr (SMALL) {
+      if (column && id == e) pair = lane;
+      t = lane / topk;
+      w = weight;
+    } else {
+      if (lane < T) {
+#pragma unroll 8
+        for (int j = topk - 1; j >= 0; --j) {
+          if (ids[j * 64 + lane] == e) {
+            pair = lane * topk + j;
+            w += weights[j * 64 + lane];
+          }
+        }
+      }
+    }
+    const uint64_t have = __ballot(pair >= 0);
+    to.token[lane] = to.pair[lane] = -1;
+    const int at = __builtin_popcountll(have & ((1ull << lane) - 1));
+    if (pair >= 0) {
+      to.token[at] = t;
+      to.pair[at] = pair;
+      to.weight[at] = w;
+    }
+    __builtin_amdgcn_wave_barrier();
+    return __builtin_popcountll(have);
+  }
+};
 
 // ------------------------------------------------------------------ gate_up
 
-template <Weights F>
+// One workgroup per chosen expert and 128 columns of y (SPLIT: 64).  Eight wavefronts own 16 rows of gate and 16 of up each,
+// over all of K; y goes out quantized.  SPLIT is for few experts, where workgroups of 128 columns would leave compute units
+// without work: pairs of wavefronts halve K, and y stays in fp32 for moe_down_kernel to quantize, since no workgroup has
+// a whole group.
+template <Weights F, bool SMALL, bool SPLIT>
 __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
-  __shared__ int ids[kMoeDecodeMaxT * kMoeDecodeMaxTopk];
-  __shared__ uint32_t bits[32];
-  __shared__ int token[64], pair[64];
+  constexpr int RW = SPLIT ? 4 : 8;
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+  __shared__ Columns cols;
+  __shared__ __attribute__((aligned(16))) float part[SPLIT ? 4 : 1][SPLIT ? 2 : 1][64][4];  // second halves of K
   __shared__ float most[8][64];
   const MoeDecodeProblem& m = p.m;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int HB = m.H / 128;
-  int a = blockIdx.x / HB;
-  const int g = blockIdx.x - a * HB;
-  chosen(m, ids, bits);
-  int e = -1;
-  for (int i = 0; i < (m.E + 31) / 32; ++i) {  // the a-th bit that is set
-    uint32_t b = bits[i];
-    const int n = __builtin_popcount(b);
-    if (a < n) {
-      for (; a > 0; --a) b &= b - 1;
-      e = 32 * i + __builtin_ctz(b);
-      break;
-    }
-    a -= n;
-  }
-  e = __builtin_amdgcn_readfirstlane(e);
-  if (e < 0) return;
-  // its tokens, in order (a token that names it twice has one column)
-  if (wave == 0) {
-    int mine = -1;
-    if (lane < m.T)
-      for (int j = m.topk - 1; j >= 0; --j)
-        if (ids[lane * m.topk + j] == e) mine = lane * m.topk + j;
-    const uint64_t have = __ballot(mine >= 0);
-    const int at = __builtin_popcountll(have & ((1ull << lane) - 1));
-    token[lane] = pair[lane] = -1;
-    if (mine >= 0) {
-      token[at] = lane;
-      pair[at] = mine;
-    }
-  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int HB = m.H / (16 * RW), a = blockIdx.x / HB, g = blockIdx.x - a * HB;
+  const int h0 = 16 * (RW * g + wave % RW), half = wave / RW;  // this wavefront's columns of y, and its half of K
+  Routing<SMALL> routing;
+  routing.open(m, lane, lds, false);
+  if (a >= routing.active) return;
+  const int e = routing.expert(a, lane);
+  // each wavefront could find the columns, but one does and all read them
+  int n = 0;
+  if (wave == 0) n = routing.columns(e, lane, cols);
   __syncthreads();
+  (void)n;
   const int KB = m.K / 128, units = (KB + 3) / 4;
+  const int u0 = SPLIT ? units * half / 2 : 0, u1 = SPLIT ? units * (half + 1) / 2 : units;
   const int c = lane >> 4, r = lane & 15;
-  const Rows<F> gate(m.w13, m.s13, e, 2 * m.H, m.K, 128 * g + 16 * wave, lane);
-  const Rows<F> up(m.w13, m.s13, e, 2 * m.H, m.K, m.H + 128 * g + 16 * wave, lane);
+  const Rows<F> gate(m.w13, m.s13, e, 2 * m.H, m.K, h0, lane);
+  const Rows<F> up(m.w13, m.s13, e, 2 * m.H, m.K, m.H + h0, lane);
   const auto rq = shared_run(m.q, (uint32_t)((m.T - 1) * m.ldq + m.K));
   const auto rs = shared_run(m.sf, (uint32_t)(((units - 1) * m.ld_sf + m.T) * 4));
 
   auto body = [&](auto cb_tag) {
     constexpr int CB = decltype(cb_tag)::value;
+    constexpr int XD = CB <= 2 ? 4 : 2;  // K-blocks of tokens ahead, as registers allow
     uint32_t q_at[CB], s_at[CB];
 #pragma unroll
     for (int b = 0; b < CB; ++b) {
-      const int t = token[16 * b + r];
+      const int t = cols.token[16 * b + r];
       q_at[b] = t < 0 ? kOut : (uint32_t)(t * m.ldq + kFirst<F> * c);
       s_at[b] = t < 0 ? kOut : (uint32_t)(t * 4);
     }
     Unit<F> wg, wu;
-    u32x4 x[4][CB][2];
+    u32x4 x[XD][CB][2];
     uint32_t xs[CB], xs_next[CB];
     v4f ag[CB], au[CB];
+    const int end = 4 * u1 < KB ? 4 * u1 : KB;
+    auto load_w = [&](int j, int i) {
+      gate.load(wg, j, i, end);
+      up.load(wu, j, i, end);
+    };
     auto load_x = [&](int j, int i) {
-      const uint32_t past = j < KB ? 0 : kOut;
+      const uint32_t past = j < end ? 0 : kOut;
 #pragma unroll
       for (int b = 0; b < CB; ++b) {
         x[i][b][0] = cached16(rq, (q_at[b] + 128 * j) | past);
@@ -228,23 +353,22 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
     auto load_xs = [&](int u) {
 #pragma unroll
       for (int b = 0; b < CB; ++b)
-        xs_next[b] = cached4(rs, u < units && s_at[b] != kOut ? s_at[b] + (uint32_t)(u * m.ld_sf * 4) : kOut);
+        xs_next[b] = cached4(rs, u < u1 && s_at[b] != kOut ? s_at[b] + (uint32_t)(u * m.ld_sf * 4) : kOut);
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      gate.load(wg, i, i);
-      up.load(wu, i, i);
-      load_x(i, i);
+      load_w(4 * u0 + i, i);
+      if (i < XD) load_x(4 * u0 + i, i);
+      if (i == 0) load_xs(u0);
+      __builtin_amdgcn_sched_barrier(0);  // in the loop's order, or its waits are for all of them
     }
-    load_xs(0);
 #pragma unroll
     for (int b = 0; b < CB; ++b) ag[b] = au[b] = v4f{0, 0, 0, 0};
-    for (int u = 0; u < units; ++u) {
+    for (int u = u0; u < u1; ++u) {
 #pragma unroll
       for (int b = 0; b < CB; ++b) xs[b] = valid_bytes(xs_next[b], KB - 4 * u);
-      load_xs(u + 1);
-      wg.begin();
-      wu.begin();
+      wg.begin(4 * u, KB);
+      wu.begin(4 * u, KB);
       auto step = [&](auto i_tag) {
         constexpr int I = decltype(i_tag)::value;
 #pragma unroll
@@ -252,232 +376,320 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
           const bf16x8 vg = rows_of<F, I>(wg, k), vu = rows_of<F, I>(wu, k);
 #pragma unroll
           for (int b = 0; b < CB; ++b) {
-            const bf16x8 vx = tokens_of(x[I][b], k, scale_of(xs[b], I));
+            const bf16x8 vx = tokens_of(x[I % XD][b], k, scale_of(xs[b], I));
             ag[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, vx, ag[b], 0, 0, 0);
             au[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, vx, au[b], 0, 0, 0);
           }
         }
-        const int j = 4 * u + 4 + I;
-        gate.load(wg, j, I);
-        up.load(wu, j, I);
-        load_x(j, I);
+        pin(ag);
+        pin(au);
+        load_w(4 * u + 4 + I, I);
+        load_x(4 * u + XD + I, I % XD);
+        if constexpr (I == 0) load_xs(u + 1);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay here: K-blocks ahead of their products
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
       step(std::integral_constant<int, 2>{});
       step(std::integral_constant<int, 3>{});
     }
-    // silu(gate) * up in fp32, and the largest magnitude of each token's 128 columns
-    float y[CB][4];
+    if constexpr (SPLIT) {
+      if (half == 1) {
 #pragma unroll
-    for (int b = 0; b < CB; ++b) {
+        for (int b = 0; b < CB; ++b) {
+          *reinterpret_cast<v4f*>(part[wave % RW][2 * b][lane]) = ag[b];
+          *reinterpret_cast<v4f*>(part[wave % RW][2 * b + 1][lane]) = au[b];
+        }
+      }
+      __syncthreads();
+      if (half == 1) return;
+#pragma unroll
+      for (int b = 0; b < CB; ++b) {
+        ag[b] += *reinterpret_cast<const v4f*>(part[wave % RW][2 * b][lane]);
+        au[b] += *reinterpret_cast<const v4f*>(part[wave % RW][2 * b + 1][lane]);
+      }
+    }
+    // silu(gate) * up in fp32
+    v4f y[CB];
+#pragma unroll
+    for (int b = 0; b < CB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[b][i] = ag[b][i] / (1.0f + expf(-ag[b][i])) * au[b][i];
-      float v = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(y[b][0]), __builtin_fabsf(y[b][1])),
-                                __builtin_fmaxf(__builtin_fabsf(y[b][2]), __builtin_fabsf(y[b][3])));
-      v = __builtin_fmaxf(v, __shfl_xor(v, 16));
-      v = __builtin_fmaxf(v, __shfl_xor(v, 32));
-      if (c == 0) most[wave][16 * b + r] = v;
-    }
-    __syncthreads();
+    if constexpr (SPLIT) {
 #pragma unroll
-    for (int b = 0; b < CB; ++b) {
-      float v = 0.0f;
+      for (int b = 0; b < CB; ++b) {
+        const int at = cols.pair[16 * b + r];
+        if (at >= 0) *reinterpret_cast<v4f*>(p.y32 + (int64_t)at * m.H + h0 + 4 * c) = y[b];
+      }
+    } else {
+      // the largest magnitude of each token's 128 columns
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v = __builtin_fmaxf(v, most[i][16 * b + r]);
-      const uint32_t byte = scale_byte(__float_as_uint(v));
-      const int at = pair[16 * b + r];
-      if (at >= 0) {
-        typedef short s16x2 __attribute__((ext_vector_type(2)));
-        const float scale = __uint_as_float(byte << 23);
-        s16x2 o = {0, 0};
-        o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, y[b][0], y[b][1], scale, false);
-        o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, y[b][2], y[b][3], scale, true);
-        *reinterpret_cast<uint32_t*>(p.y + (int64_t)at * m.H + 128 * g + 16 * wave + 4 * c) =
-            __builtin_bit_cast(uint32_t, o);
-        if (c == 0 && wave == 0) reinterpret_cast<uint8_t*>(p.y_sf)[(int64_t)at * 4 * ((HB + 3) / 4) + g] = (uint8_t)byte;
+      for (int b = 0; b < CB; ++b) {
+        float v = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(y[b][0]), __builtin_fabsf(y[b][1])),
+                                  __builtin_fmaxf(__builtin_fabsf(y[b][2]), __builtin_fabsf(y[b][3])));
+        v = __builtin_fmaxf(v, __shfl_xor(v, 16));
+        v = __builtin_fmaxf(v, __shfl_xor(v, 32));
+        if (c == 0) most[wave][16 * b + r] = v;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < CB; ++b) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v = __builtin_fmaxf(v, most[i][16 * b + r]);
+        const uint32_t byte = scale_byte(__float_as_uint(v));
+        const int at = cols.pair[16 * b + r];
+        if (at >= 0) {
+          typedef short s16x2 __attribute__((ext_vector_type(2)));
+          const float scale = __uint_as_float(byte << 23);
+          s16x2 o = {0, 0};
+          o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, y[b][0], y[b][1], scale, false);
+          o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, y[b][2], y[b][3], scale, true);
+          *reinterpret_cast<uint32_t*>(p.y + (int64_t)at * m.H + h0 + 4 * c) = __builtin_bit_cast(uint32_t, o);
+          if (c == 0 && wave == 0)
+            reinterpret_cast<uint8_t*>(p.y_sf)[(int64_t)at * 4 * ((m.H + 511) / 512) + g] = (uint8_t)byte;
+        }
       }
     }
   };
-  const int blocks = __builtin_amdgcn_readfirstlane(token[48] >= 0 ? 4 : token[32] >= 0 ? 3 : token[16] >= 0 ? 2 : 1);
-  switch (blocks) {
-    case 1: body(std::integral_constant<int, 1>{}); break;
-    case 2: body(std::integral_constant<int, 2>{}); break;
-    case 3: body(std::integral_constant<int, 3>{}); break;
-    default: body(std::integral_constant<int, 4>{}); break;
+  const int blocks = __builtin_amdgcn_readfirstlane(cols.token[48] >= 0   ? 4
+                                                    : cols.token[32] >= 0 ? 3
+                                                    : cols.token[16] >= 0 ? 2
+                                                                          : 1);
+  // SPLIT and SMALL have at most 16 and 64 columns
+  if constexpr (SPLIT) {
+    body(std::integral_constant<int, 1>{});
+  } else {
+    switch (blocks) {
+      case 1: body(std::integral_constant<int, 1>{}); break;
+      case 2: body(std::integral_constant<int, 2>{}); break;
+      case 3: body(std::integral_constant<int, 3>{}); break;
+      default: body(std::integral_constant<int, 4>{}); break;
+    }
   }
 }
 
 // ------------------------------------------------------------------ down and combine
 
-template <Weights F, int CB>
-__global__ __launch_bounds__(512) void moe_down_kernel(const MoeArgs p) {
-  __shared__ int ids[kMoeDecodeMaxT * kMoeDecodeMaxTopk];
-  __shared__ uint32_t bits[32];
-  __shared__ uint16_t list[kMoeDecodeMaxE];
-  __shared__ __attribute__((aligned(16))) float part[8][CB][64][4];
+// One workgroup per 16 output columns, over all chosen experts: its wavefronts share the list of (expert, four K-blocks)
+// in equal runs.  An expert's products have its own tokens as columns, packed together; at the end of a run of one expert
+// they are weighted and added to the wavefront's sums of the tokens in LDS, which are joined in order.  MAXC: 16-column
+// blocks that an expert can have.  Y32: y comes in fp32, and the workgroup quantizes it into LDS while its first weights
+// are on the way.
+template <Weights F, bool SMALL, bool Y32, int MAXC, int NW>
+__global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];  // sums [NW][16 MAXC tokens][16], then the routing's
+  __shared__ Columns cols[NW];
   const MoeDecodeProblem& m = p.m;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane >> 4, r = lane & 15;
   const int n0 = 16 * blockIdx.x;
   const int KB = m.H / 128, units = (KB + 3) / 4;
-  chosen(m, ids, bits);
-  for (int i = threadIdx.x; i < m.E; i += blockDim.x) {
-    if (bits[i >> 5] >> (i & 31) & 1) {
-      int rank = __builtin_popcount(bits[i >> 5] & ((1u << (i & 31)) - 1));
-      for (int k = 0; k < i >> 5; ++k) rank += __builtin_popcount(bits[k]);
-      list[rank] = (uint16_t)i;
+  v4f* const sums = reinterpret_cast<v4f*>(lds) + wave * (64 * MAXC);  // [token][4 of 4 columns]
+#pragma unroll
+  for (int i = 0; i < MAXC; ++i) sums[64 * i + lane] = v4f{0, 0, 0, 0};
+  Routing<SMALL> routing;
+  routing.open(m, lane, lds + NW * 256 * MAXC, true);
+
+  const int total = routing.active * units, i0 = total * wave / NW, i1 = total * (wave + 1) / NW;
+  const int rows_y = m.T * m.topk;
+  const auto ry = shared_run(p.y, Y32 ? 0u : (uint32_t)(rows_y * m.H));
+  const auto rs = shared_run(p.y_sf, Y32 ? 0u : (uint32_t)(rows_y * units * 4));
+  uint8_t* const yl = reinterpret_cast<uint8_t*>(lds + NW * 256 * MAXC);  // Y32: codes [pair][row_bytes], then bytes
+  uint8_t* const yl_sf = yl + rows_y * row_bytes(m.H);
+  int k = i0 / units, ua = i0 - k * units;  // the expert, and its unit whose weights are loaded
+  int e = 0, left = i1 - i0;
+  Unit<F> w;
+  if (left > 0) {
+    e = routing.expert(k, lane);
+    const Rows<F> rows(m.w2, m.s2, e, m.K, m.H, n0, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      rows.load(w, 4 * ua + i, i, KB);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  int active = 0;
-  for (int k = 0; k < (m.E + 31) / 32; ++k) active += __builtin_popcount(bits[k]);
-  active = __builtin_amdgcn_readfirstlane(active);
-  __syncthreads();
-
-  // this wavefront's units of the active experts' rows, in the experts' order
-  const int total = active * units, u0 = total * wave / 8, u1 = total * (wave + 1) / 8;
-  v4f sum[CB], acc[CB];
-#pragma unroll
-  for (int b = 0; b < CB; ++b) sum[b] = acc[b] = v4f{0, 0, 0, 0};
-  const auto ry = shared_run(p.y, (uint32_t)(m.T * m.topk * m.H));
-  const auto rs = shared_run(p.y_sf, (uint32_t)(m.T * m.topk * units * 4));
-  if (u0 < u1) {
-    // loads run one unit ahead of the products, and so does the expert that they are of
-    int k_ahead = u0 / units, ua = u0 - k_ahead * units;
-    int e_ahead = 0;
-    uint32_t row[CB];  // the pair's row of y, per token
-    auto find = [&]() {
-      e_ahead = __builtin_amdgcn_readfirstlane(list[k_ahead]);
-#pragma unroll
-      for (int b = 0; b < CB; ++b) {
-        const int t = 16 * b + r;
-        row[b] = kOut;
-        if (t < m.T)
-          for (int j = m.topk - 1; j >= 0; --j)
-            if (ids[t * m.topk + j] == e_ahead) row[b] = t * m.topk + j;
+  if constexpr (Y32) {
+    // a wavefront takes 512 columns of a pair, a lane eight
+    for (int i = wave; i < rows_y * units; i += NW) {
+      const int pair = i / units, u = i - pair * units, col = 512 * u + 8 * lane;
+      u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+      if (col < m.H) {
+        v[0] = *reinterpret_cast<const u32x4*>(p.y32 + (int64_t)pair * m.H + col);
+        v[1] = *reinterpret_cast<const u32x4*>(p.y32 + (int64_t)pair * m.H + col + 4);
       }
-    };
-    Unit<F> w;
-    u32x4 x[4][CB][2];
-    uint32_t xs[CB], xs_next[CB];
-    auto load_x = [&](int j, int i) {
+      float f[8];
 #pragma unroll
-      for (int b = 0; b < CB; ++b) {
-        const uint32_t o = row[b] == kOut || j >= KB ? kOut : row[b] * m.H + 128 * j + kFirst<F> * c;
-        x[i][b][0] = cached16(ry, o);
-        x[i][b][1] = cached16(ry, o + kSecond<F>);
-      }
-    };
-    auto load_xs = [&]() {
-#pragma unroll
-      for (int b = 0; b < CB; ++b)
-        xs_next[b] = cached4(rs, row[b] == kOut ? kOut : (row[b] * units + ua) * 4);
-    };
-    find();
-    {
-      const Rows<F> rows(m.w2, m.s2, e_ahead, m.K, m.H, n0, lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        rows.load(w, 4 * ua + i, i);
-        load_x(4 * ua + i, i);
-      }
-      load_xs();
+      for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(v[q / 4][q % 4]);
+      const uint32_t byte = group_byte(f);
+      *reinterpret_cast<u32x2*>(yl + pair * row_bytes(m.H) + col) = codes_at(f, byte);
+      if (lane % 16 == 0) yl_sf[i * 4 + lane / 16] = (uint8_t)byte;
     }
-    for (int u = u0; u < u1; ++u) {
-      const int now = ua;
-      const int e = e_ahead;
-#pragma unroll
-      for (int b = 0; b < CB; ++b) xs[b] = valid_bytes(xs_next[b], KB - 4 * now);
-      bool last = false;
-      if (++ua == units) {
-        ua = 0;
-        ++k_ahead;
-        last = true;
-        if (u + 1 < u1) find();
-      }
-      last |= u + 1 == u1;
-      const bool more = u + 1 < u1;
-      const Rows<F> rows(m.w2, m.s2, e_ahead, m.K, m.H, n0, lane);
-      if (more) load_xs();
-      w.begin();
-      auto step = [&](auto i_tag) {
-        constexpr int I = decltype(i_tag)::value;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bf16x8 v = rows_of<F, I>(w, k);
-#pragma unroll
-          for (int b = 0; b < CB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, tokens_of(x[I][b], k, scale_of(xs[b], I)), acc[b], 0, 0, 0);
-        }
-        if (more) {
-          rows.load(w, 4 * ua + I, I);
-          load_x(4 * ua + I, I);
-        }
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{});
-      step(std::integral_constant<int, 3>{});
-      if (last) {
-        // the expert's part of its tokens; the others' columns may hold what a weight that is not
-        // finite makes of zeros, and are left out
+    __syncthreads();
+  }
+  if (left > 0) {
+    while (left > 0) {
+      // this wavefront's run of expert e: units ua .. ub - 1; then the next one's first unit
+      const int ub = ua + left < units ? ua + left : units;
+      left -= ub - ua;
+      const int next = left > 0 ? routing.expert(k + 1, lane) : e;
+      const int n = routing.columns(e, lane, cols[wave]);
+      const Rows<F> rows(m.w2, m.s2, e, m.K, m.H, n0, lane), rows_next(m.w2, m.s2, next, m.K, m.H, n0, lane);
+      auto run = [&](auto cb_tag) {
+        constexpr int CB = decltype(cb_tag)::value;
+        constexpr int XD = CB <= 2 ? 4 : 2;  // K-blocks of y ahead
+        uint32_t at[CB], s_at[CB];
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
-          const int t = 16 * b + r;
-          float weight = 0.0f;
-          bool has = false;
-          if (t < m.T)
-            for (int j = 0; j < m.topk; ++j)
-              if (ids[t * m.topk + j] == e) {
-                weight += m.weights[t * m.topk + j];
-                has = true;
-              }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[b][i] = has ? __builtin_fmaf(weight, acc[b][i], sum[b][i]) : sum[b][i];
-          acc[b] = v4f{0, 0, 0, 0};
+          const int pair = cols[wave].pair[16 * b + r];
+          // (of LDS a column without a token reads the first pair's row; nothing uses its sums)
+          if constexpr (Y32) {
+            at[b] = (pair < 0 ? 0 : pair * row_bytes(m.H)) + kFirst<F> * c;
+            s_at[b] = pair < 0 ? 0 : pair * units * 4;
+          } else {
+            at[b] = pair < 0 ? kOut : (uint32_t)(pair * m.H + kFirst<F> * c);
+            s_at[b] = pair < 0 ? kOut : (uint32_t)(pair * units * 4);
+          }
         }
+        u32x4 x[XD][CB][2];
+        uint32_t xs[CB], xs_next[CB];
+        v4f acc[CB];
+        auto load_x = [&](int j, int i) {
+          [[maybe_unused]] const uint32_t past = j < 4 * ub && j < KB ? 0 : kOut;
+#pragma unroll
+          for (int b = 0; b < CB; ++b) {
+            if constexpr (Y32) {
+              const uint8_t* from = yl + at[b] + 128 * (j < 4 * ub ? j : 0);  // K-blocks past H have zeros
+              x[i][b][0] = *reinterpret_cast<const u32x4*>(from);
+              x[i][b][1] = *reinterpret_cast<const u32x4*>(from + kSecond<F>);
+            } else {
+              x[i][b][0] = cached16(ry, (at[b] + 128 * j) | past);
+              x[i][b][1] = cached16(ry, (at[b] + 128 * j + kSecond<F>) | past);
+            }
+          }
+        };
+        auto load_xs = [&](int u) {
+#pragma unroll
+          for (int b = 0; b < CB; ++b) {
+            if constexpr (Y32) xs_next[b] = *reinterpret_cast<const uint32_t*>(yl_sf + s_at[b] + 4 * (u < ub ? u : 0));
+            else xs_next[b] = cached4(rs, u < ub && s_at[b] != kOut ? s_at[b] + 4 * u : kOut);
+          }
+        };
+        load_xs(ua);
+#pragma unroll
+        for (int i = 0; i < XD; ++i) {
+          load_x(4 * ua + i, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int b = 0; b < CB; ++b) acc[b] = v4f{0, 0, 0, 0};
+        for (int u = ua; u < ub; ++u) {
+#pragma unroll
+          for (int b = 0; b < CB; ++b) xs[b] = valid_bytes(xs_next[b], KB - 4 * u);
+          w.begin(4 * u, KB);
+          const bool on = u + 1 < ub;
+          auto step = [&](auto i_tag) {
+            constexpr int I = decltype(i_tag)::value;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const bf16x8 v = rows_of<F, I>(w, q);
+#pragma unroll
+              for (int b = 0; b < CB; ++b) {
+                const bf16x8 vx = tokens_of(x[I % XD][b], q, scale_of(xs[b], I));
+                acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, vx, acc[b], 0, 0, 0);
+              }
+            }
+            pin(acc);
+            if (on) rows.load(w, 4 * u + 4 + I, I, KB);
+            else rows_next.load(w, left > 0 ? I : KB, I, KB);  // the next expert's first unit, or nothing
+            load_x(4 * u + XD + I, I % XD);
+            if constexpr (I == 0) load_xs(u + 1);
+            __builtin_amdgcn_sched_barrier(0);
+          };
+          step(std::integral_constant<int, 0>{});
+          step(std::integral_constant<int, 1>{});
+          step(std::integral_constant<int, 2>{});
+          step(std::integral_constant<int, 3>{});
+        }
+#pragma unroll
+        for (int b = 0; b < CB; ++b) {
+          const int t = cols[wave].token[16 * b + r];
+          if (t >= 0) {
+            const float weight = cols[wave].weight[16 * b + r];
+            v4f v = sums[4 * t + c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(weight, acc[b][i], v[i]);
+            sums[4 * t + c] = v;
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      };
+      if constexpr (MAXC == 1) {
+        run(std::integral_constant<int, 1>{});
+      } else if constexpr (MAXC == 2) {
+        if (n <= 16) run(std::integral_constant<int, 1>{});
+        else run(std::integral_constant<int, 2>{});
+      } else {
+        if (n <= 16) run(std::integral_constant<int, 1>{});
+        else if (n <= 32) run(std::integral_constant<int, 2>{});
+        else run(std::integral_constant<int, 4>{});
       }
+      ++k;
+      ua = 0;
+      e = next;
     }
   }
-#pragma unroll
-  for (int b = 0; b < CB; ++b) *reinterpret_cast<v4f*>(part[wave][b][lane]) = sum[b];
   __syncthreads();
-  // thread -> token and four columns (as the lanes hold them)
-  for (int i = threadIdx.x; i < CB * 64; i += 512) {
-    const int l = i & 63, t = 16 * (i >> 6) + (l & 15), n = n0 + 4 * (l >> 4);
-    if (t >= m.T) continue;
+  // thread -> token and four columns
+  for (int i = threadIdx.x; i < 4 * m.T; i += NW * 64) {
+    const int t = i >> 2, n = n0 + 4 * (i & 3);
     v4f v = {0, 0, 0, 0};
     if (m.base) {
       const u32x2 b = *reinterpret_cast<const u32x2*>(m.base + t * m.ld_base + n);
       v = v4f{bf16_lo(b[0]), bf16_hi(b[0]), bf16_lo(b[1]), bf16_hi(b[1])};
     }
-    for (int k = 0; k < 8; ++k) v += *reinterpret_cast<const v4f*>(part[k][i >> 6][l]);
+#pragma unroll
+    for (int q = 0; q < NW; ++q) v += reinterpret_cast<const v4f*>(lds)[q * (64 * MAXC) + i];
     *reinterpret_cast<u32x2*>(m.out + t * m.ld_out + n) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
   }
+}
+
+template <Weights F, bool SMALL, bool Y32>
+hipError_t launch_down(const MoeArgs& a, hipStream_t stream) {
+  const MoeDecodeProblem& m = a.m;
+  const int grid = m.K / 16;
+  const int routing = 4 * Routing<SMALL>::words(m.topk);
+  if (Y32 || m.T <= 16) {
+    const int y = Y32 ? m.T * m.topk * (row_bytes(m.H) + (m.H + 511) / 512 * 4) : 0;
+    moe_down_kernel<F, SMALL, Y32, 1, 8><<<grid, 512, 8 * 1024 + routing + y, stream>>>(a);
+  } else if constexpr (!Y32) {
+    if (m.T <= 32) moe_down_kernel<F, SMALL, Y32, 2, 4><<<grid, 256, 4 * 2048 + routing, stream>>>(a);
+    else moe_down_kernel<F, SMALL, Y32, 4, 4><<<grid, 256, 4 * 4096 + routing, stream>>>(a);
+  }
+  return hipGetLastError();
 }
 
 template <Weights F>
 hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   const MoeDecodeProblem& m = a.m;
   const int pairs = m.T * m.topk, experts = m.E < pairs ? m.E : pairs;
-  moe_gate_up_kernel<F><<<experts * (m.H / 128), 512, 0, stream>>>(a);
+  const bool small = pairs <= 64, split = splits(m);
+  const int routing = 4 * Routing<false>::words(m.topk);
+  if (split) moe_gate_up_kernel<F, true, true><<<experts * (m.H / 64), 512, 0, stream>>>(a);
+  else if (small) moe_gate_up_kernel<F, true, false><<<experts * (m.H / 128), 512, 0, stream>>>(a);
+  else moe_gate_up_kernel<F, false, false><<<experts * (m.H / 128), 512, routing, stream>>>(a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int grid = m.K / 16;
-  switch ((m.T + 15) / 16) {
-    case 1: moe_down_kernel<F, 1><<<grid, 512, 0, stream>>>(a); break;
-    case 2: moe_down_kernel<F, 2><<<grid, 512, 0, stream>>>(a); break;
-    case 3: moe_down_kernel<F, 3><<<grid, 512, 0, stream>>>(a); break;
-    default: moe_down_kernel<F, 4><<<grid, 512, 0, stream>>>(a); break;
-  }
-  return hipGetLastError();
+  if (split) return launch_down<F, true, true>(a, stream);
+  return small ? launch_down<F, true, false>(a, stream) : launch_down<F, false, false>(a, stream);
 }
 
 }  // namespace
 
 size_t moe_decode_scratch_bytes(int64_t T, int64_t topk, int64_t H) {
-  return (size_t)(T * topk) * (size_t)(H + 4 * ((H + 511) / 512));
+  const int64_t pairs = T * topk, most = 4 * pairs * H;  // in fp32 at up to 64 pairs
+  return (size_t)(pairs <= 64 ? most : pairs * (H + 4 * ((H + 511) / 512)));
 }
 
 hipError_t launch_moe_decode(const MoeDecodeProblem& p, Weights kind, void* scratch, hipStream_t stream) {
@@ -485,6 +697,7 @@ hipError_t launch_moe_decode(const MoeDecodeProblem& p, Weights kind, void* scra
   a.m = p;
   a.y = static_cast<uint8_t*>(scratch);
   a.y_sf = reinterpret_cast<uint32_t*>(a.y + (int64_t)p.T * p.topk * p.H);
+  a.y32 = static_cast<float*>(scratch);
   switch (kind) {
     case Weights::kPlain: return launch<Weights::kPlain>(a, stream);
     case Weights::kShuffled: return launch<Weights::kShuffled>(a, stream);

@@ -274,7 +274,9 @@ def check_layer(layer, got, args):
 @pytest.mark.parametrize("T,E,topk,K,H,base", [
     (1, 8, 2, 512, 256, True), (1, 4, 1, 128, 128, False), (2, 40, 8, 640, 384, True), (7, 3, 3, 1152, 128, False),
     (16, 16, 4, 512, 640, True), (17, 5, 2, 256, 1024, True), (33, 8, 2, 384, 256, False), (48, 2, 2, 256, 128, True),
-    (64, 8, 5, 512, 384, True), (64, 1, 1, 128, 256, False)])
+    (64, 8, 5, 512, 384, True), (64, 1, 1, 128, 256, False), (1, 64, 64, 256, 256, False), (3, 1000, 20, 128, 128, True),
+    (20, 5, 2, 640, 640, True), (30, 200, 4, 128, 256, False), (64, 4, 1, 256, 1152, True), (16, 16, 4, 2048, 2048, False),
+    (9, 8, 7, 1152, 640, True)])
 def test_layer(kind, T, E, topk, K, H, base):
     rng = np.random.default_rng([T, E, topk, K, H])
     layer = Layer(rng, E, K, H, kind)
