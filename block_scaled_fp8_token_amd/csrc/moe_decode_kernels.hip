@@ -41,11 +41,12 @@ struct MoeArgs {
 // the banks.
 __host__ __device__ constexpr int row_bytes(int H) { return (H + 511) / 512 * 512 + 16; }
 
-// Few experts: workgroups of 128 columns of y would not be one a compute unit, and y is small enough for every workgroup of
-// the second kernel to quantize all of it.
-bool splits(const MoeDecodeProblem& m) {
+// In how many parts the first kernel takes K.  Where few experts are chosen, workgroups of 128 columns would not be one a
+// compute unit; they take 64 or 32 then, if y is small enough for every workgroup of the second kernel to quantize all of it.
+int parts_of(const MoeDecodeProblem& m) {
   const int pairs = m.T * m.topk, experts = m.E < pairs ? m.E : pairs;
-  return pairs <= 64 && m.T <= 16 && experts * (m.H / 128) < 256 && pairs * row_bytes(m.H) <= 36864;
+  if (pairs > 64 || m.T > 16 || experts * (m.H / 128) >= 256 || pairs * row_bytes(m.H) > 36864) return 1;
+  return experts * (m.H / 64) >= 192 ? 2 : 4;
 }
 
 __device__ __forceinline__ u32x4 cached16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
@@ -110,8 +111,10 @@ struct Rows {
       if (i == 0) v.s_ahead = cached4(s, (uint32_t)(j * 64 + at / 4) | past);
     } else {
       const uint32_t o = at + j * (F == Weights::kShuffled ? 4096 : 128);
-      v.w[i][0] = run_load16(w, o | past);
-      v.w[i][1] = run_load16(w, (o + (F == Weights::kShuffled ? 2048 : 64)) | past);
+      // Plain rows come half a cache line an instruction, so the line has to stay for the other half: streaming loads took
+      // 183 us of a gate_up product of 16 tokens, these 152.
+      v.w[i][0] = F == Weights::kPlain ? cached16(w, o | past) : run_load16(w, o | past);
+      v.w[i][1] = F == Weights::kPlain ? cached16(w, (o + 64) | past) : run_load16(w, (o + 2048) | past);
       if (i == 0) v.s_ahead = cached16(s, (uint32_t)(j * 4) | past);
     }
   }
@@ -290,22 +293,23 @@ struct Routing {
 
 // ------------------------------------------------------------------ gate_up
 
-// One workgroup per chosen expert and 128 columns of y (SPLIT: 64).  Eight wavefronts own 16 rows of gate and 16 of up each,
-// over all of K; y goes out quantized.  SPLIT is for few experts, where workgroups of 128 columns would leave compute units
-// without work: pairs of wavefronts halve K, and y stays in fp32 for moe_down_kernel to quantize, since no workgroup has
-// a whole group.
-template <Weights F, bool SMALL, bool SPLIT>
+// One workgroup per chosen expert and 128 / KW columns of y.  Eight wavefronts own 16 rows of gate and 16 of up each, over a
+// KW-th of K, and share the tokens of it through LDS, where they lie as bf16, a unit of four K-blocks ahead (each wavefront
+// reading them from the L2 by itself: 163 us for 64 tokens; so 145).  With KW = 1 y goes out quantized.  The others are for
+// few experts, where workgroups of 128 columns would leave compute units without work (1 token of 8 experts of 7168 x 2048:
+// 47.2 us, with KW = 2 38.5); y stays in fp32 for moe_down_kernel to quantize, since no workgroup has a whole group.
+template <Weights F, bool SMALL, int KW>
 __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
-  constexpr int RW = SPLIT ? 4 : 8;
+  constexpr int RW = 8 / KW;
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   __shared__ Columns cols;
-  __shared__ __attribute__((aligned(16))) float part[SPLIT ? 4 : 1][SPLIT ? 2 : 1][64][4];  // second halves of K
+  __shared__ __attribute__((aligned(16))) float rest[KW == 1 ? 1 : KW - 1][RW][2][64][4];  // the other parts of K
   __shared__ float most[8][64];
   const MoeDecodeProblem& m = p.m;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int HB = m.H / (16 * RW), a = blockIdx.x / HB, g = blockIdx.x - a * HB;
-  const int h0 = 16 * (RW * g + wave % RW), half = wave / RW;  // this wavefront's columns of y, and its half of K
+  const int h0 = 16 * (RW * g + wave % RW), part = wave / RW;  // this wavefront's columns of y, and its part of K
   Routing<SMALL> routing;
   routing.open(m, lane, lds, false);
   if (a >= routing.active) return;
@@ -316,7 +320,7 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
   __syncthreads();
   (void)n;
   const int KB = m.K / 128, units = (KB + 3) / 4;
-  const int u0 = SPLIT ? units * half / 2 : 0, u1 = SPLIT ? units * (half + 1) / 2 : units;
+  const int u0 = units * part / KW, u1 = units * (part + 1) / KW;
   const int c = lane >> 4, r = lane & 15;
   const Rows<F> gate(m.w13, m.s13, e, 2 * m.H, m.K, h0, lane);
   const Rows<F> up(m.w13, m.s13, e, 2 * m.H, m.K, m.H + h0, lane);
@@ -325,58 +329,76 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
 
   auto body = [&](auto cb_tag) {
     constexpr int CB = decltype(cb_tag)::value;
-    constexpr int XD = CB <= 2 ? 4 : 2;  // K-blocks of tokens ahead, as registers allow
-    uint32_t q_at[CB], s_at[CB];
+    constexpr int GT = 512 / KW;           // threads that bring the tokens of one part of K
+    constexpr int P = CB * 512 / GT;       // pieces of 16 codes that a thread brings
+    constexpr bool DOUBLE = CB <= 2;       // two units of tokens in LDS
+    constexpr int XB = 4 * 16 * CB * 256;  // bytes of one: [block][token][16 chunks of 8 columns, chunk k at k ^ token % 16]
+    uint8_t* const xl = reinterpret_cast<uint8_t*>(lds + Routing<SMALL>::words(m.topk)) + part * (2 * XB);
+    const int at0 = threadIdx.x % GT;
+    uint32_t q_at[P], s_at[P];
 #pragma unroll
-    for (int b = 0; b < CB; ++b) {
-      const int t = cols.token[16 * b + r];
-      q_at[b] = t < 0 ? kOut : (uint32_t)(t * m.ldq + kFirst<F> * c);
-      s_at[b] = t < 0 ? kOut : (uint32_t)(t * 4);
+    for (int i = 0; i < P; ++i) {
+      const int t = cols.token[(i * GT + at0) >> 5];
+      q_at[i] = t < 0 ? kOut : (uint32_t)(t * m.ldq + 16 * (at0 & 31));
+      s_at[i] = t < 0 ? kOut : (uint32_t)(t * 4);
     }
     Unit<F> wg, wu;
-    u32x4 x[XD][CB][2];
-    uint32_t xs[CB], xs_next[CB];
+    u32x4 xq[P];
+    uint32_t xs[P];
     v4f ag[CB], au[CB];
     const int end = 4 * u1 < KB ? 4 * u1 : KB;
     auto load_w = [&](int j, int i) {
       gate.load(wg, j, i, end);
       up.load(wu, j, i, end);
     };
-    auto load_x = [&](int j, int i) {
-      const uint32_t past = j < end ? 0 : kOut;
+    auto load_x = [&](int u) {
 #pragma unroll
-      for (int b = 0; b < CB; ++b) {
-        x[i][b][0] = cached16(rq, (q_at[b] + 128 * j) | past);
-        x[i][b][1] = cached16(rq, (q_at[b] + 128 * j + kSecond<F>) | past);
+      for (int i = 0; i < P; ++i) {
+        const bool out = q_at[i] == kOut || 4 * u + ((at0 & 31) >> 3) >= end;
+        xq[i] = cached16(rq, out ? kOut : q_at[i] + 512 * u);
+        xs[i] = cached4(rs, out ? kOut : s_at[i] + (uint32_t)(u * m.ld_sf * 4));
       }
     };
-    auto load_xs = [&](int u) {
+    // as bf16 with their scale (exact), eight columns a chunk
+    auto store_x = [&](int buf) {
 #pragma unroll
-      for (int b = 0; b < CB; ++b)
-        xs_next[b] = cached4(rs, u < u1 && s_at[b] != kOut ? s_at[b] + (uint32_t)(u * m.ld_sf * 4) : kOut);
+      for (int i = 0; i < P; ++i) {
+        const int t = (i * GT + at0) >> 5, piece = at0 & 31, block = piece >> 3, chunk = 2 * (piece & 7);
+        const float scale = scale_of(xs[i], block);
+        uint8_t* row = xl + (DOUBLE ? buf * XB : 0) + (block * 16 * CB + t) * 256;
+        *reinterpret_cast<bf16x8*>(row + ((chunk ^ (t & 15)) << 4)) = from_e4m3(xq[i][0], xq[i][1], scale);
+        *reinterpret_cast<bf16x8*>(row + (((chunk + 1) ^ (t & 15)) << 4)) = from_e4m3(xq[i][2], xq[i][3], scale);
+      }
     };
+    load_x(u0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       load_w(4 * u0 + i, i);
-      if (i < XD) load_x(4 * u0 + i, i);
-      if (i == 0) load_xs(u0);
       __builtin_amdgcn_sched_barrier(0);  // in the loop's order, or its waits are for all of them
     }
+    store_x(0);
+    __syncthreads();
 #pragma unroll
     for (int b = 0; b < CB; ++b) ag[b] = au[b] = v4f{0, 0, 0, 0};
-    for (int u = u0; u < u1; ++u) {
-#pragma unroll
-      for (int b = 0; b < CB; ++b) xs[b] = valid_bytes(xs_next[b], KB - 4 * u);
+    // (all parts take as many turns, the shorter ones' last over zeros)
+    const int turns = (units + KW - 1) / KW;
+    for (int n = 0; n < turns; ++n) {
+      const int u = u0 + n;
+      load_x(u + 1);
+      __builtin_amdgcn_sched_barrier(0);
       wg.begin(4 * u, KB);
       wu.begin(4 * u, KB);
       auto step = [&](auto i_tag) {
         constexpr int I = decltype(i_tag)::value;
+        const uint8_t* from = xl + (DOUBLE ? (n & 1) * XB : 0) + I * 16 * CB * 256;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const bf16x8 vg = rows_of<F, I>(wg, k), vu = rows_of<F, I>(wu, k);
+          const int chunk = F == Weights::kW4 ? 4 * c + k : 8 * (k >> 1) + 2 * c + (k & 1);
 #pragma unroll
           for (int b = 0; b < CB; ++b) {
-            const bf16x8 vx = tokens_of(x[I % XD][b], k, scale_of(xs[b], I));
+            const bf16x8 vx = *reinterpret_cast<const bf16x8*>(from + ((16 * b + r) * 16 + (chunk ^ r)) * 16);
             ag[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vg, vx, ag[b], 0, 0, 0);
             au[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vu, vx, au[b], 0, 0, 0);
           }
@@ -384,29 +406,28 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
         pin(ag);
         pin(au);
         load_w(4 * u + 4 + I, I);
-        load_x(4 * u + XD + I, I % XD);
-        if constexpr (I == 0) load_xs(u + 1);
-        __builtin_amdgcn_sched_barrier(0);  // the loads stay here: K-blocks ahead of their products
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay here: four K-blocks ahead of their products
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
       step(std::integral_constant<int, 2>{});
       step(std::integral_constant<int, 3>{});
+      if constexpr (!DOUBLE) __syncthreads();
+      store_x((n + 1) & 1);
+      __syncthreads();
     }
-    if constexpr (SPLIT) {
-      if (half == 1) {
-#pragma unroll
-        for (int b = 0; b < CB; ++b) {
-          *reinterpret_cast<v4f*>(part[wave % RW][2 * b][lane]) = ag[b];
-          *reinterpret_cast<v4f*>(part[wave % RW][2 * b + 1][lane]) = au[b];
-        }
+    if constexpr (KW > 1) {
+      static_assert(CB == 1);
+      if (part > 0) {
+        *reinterpret_cast<v4f*>(rest[part - 1][wave % RW][0][lane]) = ag[0];
+        *reinterpret_cast<v4f*>(rest[part - 1][wave % RW][1][lane]) = au[0];
       }
       __syncthreads();
-      if (half == 1) return;
+      if (part > 0) return;
 #pragma unroll
-      for (int b = 0; b < CB; ++b) {
-        ag[b] += *reinterpret_cast<const v4f*>(part[wave % RW][2 * b][lane]);
-        au[b] += *reinterpret_cast<const v4f*>(part[wave % RW][2 * b + 1][lane]);
+      for (int i = 0; i < KW - 1; ++i) {
+        ag[0] += *reinterpret_cast<const v4f*>(rest[i][wave][0][lane]);
+        au[0] += *reinterpret_cast<const v4f*>(rest[i][wave][1][lane]);
       }
     }
     // silu(gate) * up in fp32
@@ -415,7 +436,7 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
     for (int b = 0; b < CB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[b][i] = ag[b][i] / (1.0f + expf(-ag[b][i])) * au[b][i];
-    if constexpr (SPLIT) {
+    if constexpr (KW > 1) {
 #pragma unroll
       for (int b = 0; b < CB; ++b) {
         const int at = cols.pair[16 * b + r];
@@ -456,8 +477,7 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
                                                     : cols.token[32] >= 0 ? 3
                                                     : cols.token[16] >= 0 ? 2
                                                                           : 1);
-  // SPLIT and SMALL have at most 16 and 64 columns
-  if constexpr (SPLIT) {
+  if constexpr (KW > 1) {  // for at most 16 tokens
     body(std::integral_constant<int, 1>{});
   } else {
     switch (blocks) {
@@ -471,42 +491,45 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
 
 // ------------------------------------------------------------------ down and combine
 
-// One workgroup per 16 output columns, over all chosen experts: its wavefronts share the list of (expert, four K-blocks)
+// One workgroup per 16 RT output columns, over all chosen experts: its wavefronts share the list of (expert, four K-blocks)
 // in equal runs.  An expert's products have its own tokens as columns, packed together; at the end of a run of one expert
 // they are weighted and added to the wavefront's sums of the tokens in LDS, which are joined in order.  MAXC: 16-column
 // blocks that an expert can have.  Y32: y comes in fp32, and the workgroup quantizes it into LDS while its first weights
 // are on the way.
-template <Weights F, bool SMALL, bool Y32, int MAXC, int NW>
+template <Weights F, bool SMALL, bool Y32, int MAXC, int NW, int RT>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
-  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];  // sums [NW][16 MAXC tokens][16], then the routing's
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];  // sums [NW][16 MAXC tokens][16 RT], then the routing's
   __shared__ Columns cols[NW];
   const MoeDecodeProblem& m = p.m;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane >> 4, r = lane & 15;
-  const int n0 = 16 * blockIdx.x;
+  const int n0 = 16 * RT * blockIdx.x;
   const int KB = m.H / 128, units = (KB + 3) / 4;
-  v4f* const sums = reinterpret_cast<v4f*>(lds) + wave * (64 * MAXC);  // [token][4 of 4 columns]
+  v4f* const sums = reinterpret_cast<v4f*>(lds) + wave * (64 * MAXC * RT);  // [token][4 RT of 4 columns]
 #pragma unroll
-  for (int i = 0; i < MAXC; ++i) sums[64 * i + lane] = v4f{0, 0, 0, 0};
+  for (int i = 0; i < MAXC * RT; ++i) sums[64 * i + lane] = v4f{0, 0, 0, 0};
   Routing<SMALL> routing;
-  routing.open(m, lane, lds + NW * 256 * MAXC, true);
+  routing.open(m, lane, lds + NW * 256 * MAXC * RT, true);
 
   const int total = routing.active * units, i0 = total * wave / NW, i1 = total * (wave + 1) / NW;
   const int rows_y = m.T * m.topk;
   const auto ry = shared_run(p.y, Y32 ? 0u : (uint32_t)(rows_y * m.H));
   const auto rs = shared_run(p.y_sf, Y32 ? 0u : (uint32_t)(rows_y * units * 4));
-  uint8_t* const yl = reinterpret_cast<uint8_t*>(lds + NW * 256 * MAXC);  // Y32: codes [pair][row_bytes], then bytes
+  uint8_t* const yl = reinterpret_cast<uint8_t*>(lds + NW * 256 * MAXC * RT);  // Y32: codes [pair][row_bytes], then bytes
   uint8_t* const yl_sf = yl + rows_y * row_bytes(m.H);
   int k = i0 / units, ua = i0 - k * units;  // the expert, and its unit whose weights are loaded
   int e = 0, left = i1 - i0;
-  Unit<F> w;
+  Unit<F> w[RT];
+  auto load_w = [&](int of, int j, int i) {
+#pragma unroll
+    for (int q = 0; q < RT; ++q) Rows<F>(m.w2, m.s2, of, m.K, m.H, n0 + 16 * q, lane).load(w[q], j, i, KB);
+  };
   if (left > 0) {
     e = routing.expert(k, lane);
-    const Rows<F> rows(m.w2, m.s2, e, m.K, m.H, n0, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      rows.load(w, 4 * ua + i, i, KB);
+      load_w(e, 4 * ua + i, i);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -535,10 +558,9 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
       left -= ub - ua;
       const int next = left > 0 ? routing.expert(k + 1, lane) : e;
       const int n = routing.columns(e, lane, cols[wave]);
-      const Rows<F> rows(m.w2, m.s2, e, m.K, m.H, n0, lane), rows_next(m.w2, m.s2, next, m.K, m.H, n0, lane);
       auto run = [&](auto cb_tag) {
         constexpr int CB = decltype(cb_tag)::value;
-        constexpr int XD = CB <= 2 ? 4 : 2;  // K-blocks of y ahead
+        constexpr int XD = CB <= 2 ? 4 : 1;  // K-blocks of y ahead, as registers allow
         uint32_t at[CB], s_at[CB];
 #pragma unroll
         for (int b = 0; b < CB; ++b) {
@@ -554,7 +576,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
         }
         u32x4 x[XD][CB][2];
         uint32_t xs[CB], xs_next[CB];
-        v4f acc[CB];
+        v4f acc[RT][CB];
         auto load_x = [&](int j, int i) {
           [[maybe_unused]] const uint32_t past = j < 4 * ub && j < KB ? 0 : kOut;
 #pragma unroll
@@ -583,26 +605,33 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int b = 0; b < CB; ++b) acc[b] = v4f{0, 0, 0, 0};
+        for (int i = 0; i < RT * CB; ++i) acc[i / CB][i % CB] = v4f{0, 0, 0, 0};
         for (int u = ua; u < ub; ++u) {
 #pragma unroll
           for (int b = 0; b < CB; ++b) xs[b] = valid_bytes(xs_next[b], KB - 4 * u);
-          w.begin(4 * u, KB);
+#pragma unroll
+          for (int q = 0; q < RT; ++q) w[q].begin(4 * u, KB);
+          // ahead: this expert's next unit, the next expert's first, or nothing (no branch, so that the waits are for as few
+          // loads as have to be)
           const bool on = u + 1 < ub;
+          const int e_ahead = on ? e : next, j_ahead = on ? 4 * u + 4 : left > 0 ? 0 : KB;
           auto step = [&](auto i_tag) {
             constexpr int I = decltype(i_tag)::value;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const bf16x8 v = rows_of<F, I>(w, q);
+            for (int k4 = 0; k4 < 4; ++k4) {
+              bf16x8 v[RT];
+#pragma unroll
+              for (int q = 0; q < RT; ++q) v[q] = rows_of<F, I>(w[q], k4);
 #pragma unroll
               for (int b = 0; b < CB; ++b) {
-                const bf16x8 vx = tokens_of(x[I % XD][b], q, scale_of(xs[b], I));
-                acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, vx, acc[b], 0, 0, 0);
+                const bf16x8 vx = tokens_of(x[I % XD][b], k4, scale_of(xs[b], I));
+#pragma unroll
+                for (int q = 0; q < RT; ++q) acc[q][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[q], vx, acc[q][b], 0, 0, 0);
               }
             }
-            pin(acc);
-            if (on) rows.load(w, 4 * u + 4 + I, I, KB);
-            else rows_next.load(w, left > 0 ? I : KB, I, KB);  // the next expert's first unit, or nothing
+#pragma unroll
+            for (int q = 0; q < RT; ++q) pin(acc[q]);
+            load_w(e_ahead, j_ahead + I, I);
             load_x(4 * u + XD + I, I % XD);
             if constexpr (I == 0) load_xs(u + 1);
             __builtin_amdgcn_sched_barrier(0);
@@ -617,10 +646,13 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
           const int t = cols[wave].token[16 * b + r];
           if (t >= 0) {
             const float weight = cols[wave].weight[16 * b + r];
-            v4f v = sums[4 * t + c];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(weight, acc[b][i], v[i]);
-            sums[4 * t + c] = v;
+            for (int q = 0; q < RT; ++q) {
+              v4f v = sums[4 * (RT * t + q) + c];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(weight, acc[q][b][i], v[i]);
+              sums[4 * (RT * t + q) + c] = v;
+            }
           }
         }
         __builtin_amdgcn_wave_barrier();
@@ -642,30 +674,31 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(const MoeArgs p) {
   }
   __syncthreads();
   // thread -> token and four columns
-  for (int i = threadIdx.x; i < 4 * m.T; i += NW * 64) {
-    const int t = i >> 2, n = n0 + 4 * (i & 3);
+  for (int i = threadIdx.x; i < 4 * RT * m.T; i += NW * 64) {
+    const int t = i / (4 * RT), n = n0 + 4 * (i % (4 * RT));
     v4f v = {0, 0, 0, 0};
     if (m.base) {
       const u32x2 b = *reinterpret_cast<const u32x2*>(m.base + t * m.ld_base + n);
       v = v4f{bf16_lo(b[0]), bf16_hi(b[0]), bf16_lo(b[1]), bf16_hi(b[1])};
     }
 #pragma unroll
-    for (int q = 0; q < NW; ++q) v += reinterpret_cast<const v4f*>(lds)[q * (64 * MAXC) + i];
+    for (int q = 0; q < NW; ++q) v += reinterpret_cast<const v4f*>(lds)[q * (64 * MAXC * RT) + i];
     *reinterpret_cast<u32x2*>(m.out + t * m.ld_out + n) = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
   }
 }
 
-template <Weights F, bool SMALL, bool Y32>
+template <Weights F, bool SMALL, bool Y32, int RT>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream) {
   const MoeDecodeProblem& m = a.m;
-  const int grid = m.K / 16;
-  const int routing = 4 * Routing<SMALL>::words(m.topk);
-  if (Y32 || m.T <= 16) {
-    const int y = Y32 ? m.T * m.topk * (row_bytes(m.H) + (m.H + 511) / 512 * 4) : 0;
-    moe_down_kernel<F, SMALL, Y32, 1, 8><<<grid, 512, 8 * 1024 + routing + y, stream>>>(a);
-  } else if constexpr (!Y32) {
-    if (m.T <= 32) moe_down_kernel<F, SMALL, Y32, 2, 4><<<grid, 256, 4 * 2048 + routing, stream>>>(a);
-    else moe_down_kernel<F, SMALL, Y32, 4, 4><<<grid, 256, 4 * 4096 + routing, stream>>>(a);
+  constexpr int NW = 8;
+  const int grid = m.K / (16 * RT), routing = 4 * Routing<SMALL>::words(m.topk), sums = NW * 1024 * RT;
+  if constexpr (Y32) {
+    const int y = m.T * m.topk * (row_bytes(m.H) + (m.H + 511) / 512 * 4);
+    moe_down_kernel<F, SMALL, Y32, 1, NW, RT><<<grid, 512, sums + routing + y, stream>>>(a);
+  } else {
+    if (m.T <= 16) moe_down_kernel<F, SMALL, Y32, 1, NW, RT><<<grid, 512, sums + routing, stream>>>(a);
+    else if (m.T <= 32) moe_down_kernel<F, SMALL, Y32, 2, NW, RT><<<grid, 512, 2 * sums + routing, stream>>>(a);
+    else moe_down_kernel<F, SMALL, Y32, 4, NW, RT><<<grid, 512, 4 * sums + routing, stream>>>(a);
   }
   return hipGetLastError();
 }
@@ -673,23 +706,28 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t stream) {
 template <Weights F>
 hipError_t launch(const MoeArgs& a, hipStream_t stream) {
   const MoeDecodeProblem& m = a.m;
-  const int pairs = m.T * m.topk, experts = m.E < pairs ? m.E : pairs;
-  const bool small = pairs <= 64, split = splits(m);
-  const int routing = 4 * Routing<false>::words(m.topk);
-  if (split) moe_gate_up_kernel<F, true, true><<<experts * (m.H / 64), 512, 0, stream>>>(a);
-  else if (small) moe_gate_up_kernel<F, true, false><<<experts * (m.H / 128), 512, 0, stream>>>(a);
-  else moe_gate_up_kernel<F, false, false><<<experts * (m.H / 128), 512, routing, stream>>>(a);
+  const int pairs = m.T * m.topk, experts = m.E < pairs ? m.E : pairs, KW = parts_of(m);
+  const bool small = pairs <= 64;
+  // two units of tokens for up to two blocks of 16, or one for up to four
+  const int routing = 4 * Routing<false>::words(m.topk), tokens = m.T <= 16 ? 32768 : 65536;
+  if (KW == 4) moe_gate_up_kernel<F, true, 4><<<experts * (m.H / 32), 512, 4 * 32768, stream>>>(a);
+  else if (KW == 2) moe_gate_up_kernel<F, true, 2><<<experts * (m.H / 64), 512, 2 * 32768, stream>>>(a);
+  else if (small) moe_gate_up_kernel<F, true, 1><<<experts * (m.H / 128), 512, tokens, stream>>>(a);
+  else moe_gate_up_kernel<F, false, 1><<<experts * (m.H / 128), 512, routing + tokens, stream>>>(a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  if (split) return launch_down<F, true, true>(a, stream);
-  return small ? launch_down<F, true, false>(a, stream) : launch_down<F, false, false>(a, stream);
+  if (KW > 1) return launch_down<F, true, true, 1>(a, stream);
+  // 32 output columns a workgroup, for the tokens that both halves then share (16 tokens of 32 experts: 83.5 us with 16
+  // columns, 71.4), unless 16 still leave compute units without one
+  if (m.K / 16 <= 256) return small ? launch_down<F, true, false, 1>(a, stream) : launch_down<F, false, false, 1>(a, stream);
+  return small ? launch_down<F, true, false, 2>(a, stream) : launch_down<F, false, false, 2>(a, stream);
 }
 
 }  // namespace
 
 size_t moe_decode_scratch_bytes(int64_t T, int64_t topk, int64_t H) {
-  const int64_t pairs = T * topk, most = 4 * pairs * H;  // in fp32 at up to 64 pairs
-  return (size_t)(pairs <= 64 ? most : pairs * (H + 4 * ((H + 511) / 512)));
+  const int64_t pairs = T * topk, quantized = pairs * (H + 4 * ((H + 511) / 512));
+  return (size_t)(pairs <= 64 && 4 * pairs * H > quantized ? 4 * pairs * H : quantized);  // up to 64 pairs may be in fp32
 }
 
 hipError_t launch_moe_decode(const MoeDecodeProblem& p, Weights kind, void* scratch, hipStream_t stream) {

@@ -276,7 +276,8 @@ def check_layer(layer, got, args):
     (16, 16, 4, 512, 640, True), (17, 5, 2, 256, 1024, True), (33, 8, 2, 384, 256, False), (48, 2, 2, 256, 128, True),
     (64, 8, 5, 512, 384, True), (64, 1, 1, 128, 256, False), (1, 64, 64, 256, 256, False), (3, 1000, 20, 128, 128, True),
     (20, 5, 2, 640, 640, True), (30, 200, 4, 128, 256, False), (64, 4, 1, 256, 1152, True), (16, 16, 4, 2048, 2048, False),
-    (9, 8, 7, 1152, 640, True)])
+    (9, 8, 7, 1152, 640, True), (1, 4, 2, 4224, 1152, True), (2, 8, 8, 4224, 256, False), (12, 12, 5, 4352, 128, True),
+    (24, 4, 2, 4224, 128, False), (40, 6, 3, 4352, 256, True), (64, 2, 1, 4224, 128, False), (1, 16, 12, 640, 2048, True)])
 def test_layer(kind, T, E, topk, K, H, base):
     rng = np.random.default_rng([T, E, topk, K, H])
     layer = Layer(rng, E, K, H, kind)
