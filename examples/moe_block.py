@@ -9,7 +9,8 @@
 
 and back: every activation's gradient, and those of the norms' weights, the gates and the
 router.  (The experts' own weights have their gradients as products over the tokens, which
-the library has no kernel for.)
+the library has no kernel for.)  For the few tokens of a decode step the experts' part is one
+call (moe_decode_layer).
 
     python examples/moe_block.py [--tokens 512] [--hidden 1024] [--half 512] [--experts 16] [--topk 4]
 """
@@ -73,6 +74,16 @@ class MoeBlock:
         kept = dict(y=y, h=h, logits=logits, ids=ids, w=w, rows=rows, slots=slots, cq=cq, csf=csf, experts=experts,
                     out=out, h1=h1)
         return h1, q, sf, kept
+
+    def decode(self, x, y):
+        """The same block for the few tokens of a decode step: at most 64, none dropped -> the new stream and the next
+        block's input in e4m3 (codes, scale words)."""
+        n, g = self.norms, self.gates
+        h, z, q, sf = F.residual_rms_norm(x, n["pre0"], y=y, w_post=n["post0"], gate=g["gate0"], out="both")
+        ids, w = F.moe_route_topk(torch.mm(z, self.router.t()), self.topk, bias=self.bias, **self.route)
+        out = F.moe_decode_layer(q, sf, ids, w, *self.gate_up, *self.down)
+        h1, _, q, sf = F.residual_rms_norm(h, n["pre1"], y=out, w_post=n["post1"], gate=g["gate1"], out="fp8")
+        return h1, q, sf
 
     def backward(self, d_h1, d_z1, s):
         """Gradients of the new stream and of the next block's input -> those of x and y, and of the weights
