@@ -27,8 +27,15 @@ struct Block {
 
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rz, int q,
                                        int j, uint32_t past, int KB, uint32_t s_tile, uint32_t z_tile, int lane) {
-    const uint32_t u = (uint32_t)j >> 2, k = (uint32_t)j & 3, r = lane & 15;
+    load_codes(rw, q, j, past, KB, lane);
+    load_scales(rs, rz, q, j, past, s_tile, z_tile, lane);
+  }
+  __device__ __forceinline__ void load_codes(__amdgpu_buffer_rsrc_t rw, int q, int j, uint32_t past, int KB, int lane) {
     w = run_load16(rw, (uint32_t)((q * KB + j) * 1024 + 16 * lane) | past);
+  }
+  __device__ __forceinline__ void load_scales(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rz, int q, int j,
+                                              uint32_t past, uint32_t s_tile, uint32_t z_tile, int lane) {
+    const uint32_t u = (uint32_t)j >> 2, k = (uint32_t)j & 3, r = lane & 15;
     if constexpr (E2M1) {
       s[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)((q * s_tile + u * 256 + 4 * lane + k) | past), 0, 0);
     } else {
@@ -76,6 +83,50 @@ struct Block {
   }
   __device__ __forceinline__ float scale(int g) const { return g & 1 ? bf16_hi(s[g / 2]) : bf16_lo(s[g / 2]); }
   __device__ __forceinline__ float zero(int g) const { return (float)((z >> (8 * g)) & 0xFF); }
+};
+
+// The scales (and zero points) of a unit of four K-blocks of one tile, as they lie side by side: one or two loads where each
+// K-block's own took four to eight.
+template <int GP, bool Z>
+struct UnitScales {
+  static constexpr int NS = GP == 0 ? 1 : 2 * GP, NZ = Z ? GP : 1;
+  uint32_t s[NS], z[NZ];
+
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rz, uint32_t s_at, uint32_t z_at,
+                                       int u, uint32_t past, int lane) {
+    const uint32_t at = (s_at + (GP == 0 ? u * 256 + 4 * lane : (u * 16 + (lane & 15)) * 8 * GP)) | past;
+    words<NS>(s, rs, at);
+    if constexpr (Z) words<NZ>(z, rz, (z_at + (u * 16 + (lane & 15)) * 4 * GP) | past);
+  }
+  template <int N>
+  static __device__ __forceinline__ void words(uint32_t (&to)[N], __amdgpu_buffer_rsrc_t r, uint32_t at) {
+    if constexpr (N == 1) {
+      to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 0);
+    } else if constexpr (N == 2) {
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0));
+      to[0] = v[0];
+      to[1] = v[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(at + 4 * i), 0, 0));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[i + k] = v[k];
+      }
+    }
+  }
+  // Those of K-block I.
+  template <int I>
+  __device__ __forceinline__ void give(Block<GP, Z>& b) const {
+    if constexpr (GP == 0) b.s[0] = s[0] >> (8 * I);
+    if constexpr (GP == 1) b.s[0] = s[I / 2] >> (16 * (I & 1));
+    if constexpr (GP == 2) b.s[0] = s[I];
+    if constexpr (GP == 4) {
+      b.s[0] = s[2 * I];
+      b.s[1] = s[2 * I + 1];
+    }
+    if constexpr (Z) b.z = GP == 4 ? z[I % NZ] : GP == 2 ? z[I / 2 % NZ] >> (16 * (I & 1)) : z[0] >> (8 * I);
+  }
 };
 
 __device__ __forceinline__ bf16x8 eight_of(float v) {
@@ -139,7 +190,8 @@ __device__ __forceinline__ void multiply(v4f (&acc)[RT], const bf16x8 (&x)[4], c
 template <int GP, bool Z, int SL, int CB, int RT, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) {
   constexpr bool E2M1 = GP == 0;
-  constexpr int D = CB <= 2 ? 4 : 2;  // K-blocks ahead
+  constexpr int D = CB == 1 ? 4 : 2;  // K-blocks ahead, as registers allow (more spills: 20 tokens 30 us against 17)
+  constexpr bool UNITS = CB <= 2;     // scales a unit at a time; with more tokens its registers are wanted elsewhere
   constexpr int TS = 16 / SL;         // tokens a slot
   __shared__ __attribute__((aligned(16))) float part[NW][CB * RT][64][4];
   const int lane = threadIdx.x & 63;
@@ -160,8 +212,16 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) 
     x_at[b] = 16 * b + r % TS < T ? (uint32_t)((16 * b + r % TS) * p.ldx * 2) + (E2M1 ? 64 * c : 16 * c) + 256 * (r / TS)
                                  : kOut;
 
-  const int j0 = KB * wave / NW, j1 = KB * (wave + 1) / NW;
+  // this wavefront's K-blocks: whole units of four where there are enough of them
+  int j0 = KB * wave / NW, j1 = KB * (wave + 1) / NW;
+  if (units >= NW) {
+    j0 = 4 * (units * wave / NW);
+    j1 = 4 * (units * (wave + 1) / NW);
+    j1 = j1 < KB ? j1 : KB;
+  }
+  const int first = j0 & ~3;
   Block<GP, Z> w[D][RT];
+  UnitScales<GP, Z> scales[RT], scales_ahead[RT];
   bf16x8 x[D / SL][CB][4], x_ahead[CB][4];
   v4f acc[CB][SL][RT];
 #pragma unroll
@@ -169,13 +229,21 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) 
 #pragma unroll
     for (int i = 0; i < SL * RT; ++i) acc[b][i / RT][i % RT] = v4f{0, 0, 0, 0};
   auto load_w = [&](int j, int i) {
+    const uint32_t past = j >= j0 && j < j1 ? 0 : kOut;
 #pragma unroll
-    for (int q = 0; q < RT; ++q) w[i][q].load(rw, rs, rz, q, j, j < j1 ? 0 : kOut, KB, s_tile, z_tile, lane);
+    for (int q = 0; q < RT; ++q) {
+      w[i][q].load_codes(rw, q, j, past, KB, lane);
+      if constexpr (!UNITS) w[i][q].load_scales(rs, rz, q, j, past, s_tile, z_tile, lane);
+    }
+  };
+  auto load_s = [&](int j) {
+#pragma unroll
+    for (int q = 0; UNITS && q < RT; ++q) scales_ahead[q].load(rs, rz, q * s_tile, q * z_tile, j >> 2, j < j1 ? 0 : kOut, lane);
   };
   // tokens of the SL K-blocks from j; a slot past the range has zeros (what lies there is the next token's, and a value
   // of it that is not finite would not vanish against weights of zero)
   auto load_x = [&](int j, bf16x8(&to)[CB][4]) {
-    const uint32_t past = j + r / TS < j1 ? 0 : kOut;
+    const uint32_t past = j + r / TS >= j0 && j + r / TS < j1 ? 0 : kOut;
 #pragma unroll
     for (int b = 0; b < CB; ++b)
 #pragma unroll
@@ -185,30 +253,35 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) 
   };
 #pragma unroll
   for (int i = 0; i < D; ++i) {
-    load_w(j0 + i, i);
-    if (i % SL == 0) load_x(j0 + i, x[i / SL]);
+    load_w(first + i, i);
+    if (i % SL == 0) load_x(first + i, x[i / SL]);
+    if (i == 0) load_s(first);
     __builtin_amdgcn_sched_barrier(0);  // in the loop's order, or its waits are for all of them
   }
   auto step = [&](int j, auto i_tag) {
-    constexpr int I = decltype(i_tag)::value, IX = I / SL, S = I % SL;
+    constexpr int I = decltype(i_tag)::value, IX = I % D / SL, S = I % SL;
     if constexpr (SL == D && S == 0) load_x(j + D, x_ahead);
+    if constexpr (I == 0) load_s(j + 4);
     bf16x8 v[RT][4];
 #pragma unroll
-    for (int q = 0; q < RT; ++q) w[I][q].decode(v[q]);
+    for (int q = 0; q < RT; ++q) {
+      if constexpr (UNITS) scales[q].template give<I>(w[I % D][q]);
+      w[I % D][q].decode(v[q]);
+    }
 #pragma unroll
-    for (int b = 0; b < CB; ++b) multiply<GP, Z, RT>(acc[b][S], x[IX][b], w[I], v);
-    load_w(j + D, I);
+    for (int b = 0; b < CB; ++b) multiply<GP, Z, RT>(acc[b][S], x[IX][b], w[I % D], v);
+    load_w(j + D, I % D);
     if constexpr (SL < D && S == SL - 1) load_x(j - S + D, x[IX]);
     __builtin_amdgcn_sched_barrier(0);  // the loads stay here: D K-blocks ahead of their products
   };
-  for (int j = j0; j < j1; j += D) {
-    // K-blocks past the range have weights and tokens of zeros
+  for (int j = first; j < j1; j += 4) {
+    // K-blocks outside the range have weights and tokens of zeros
+#pragma unroll
+    for (int q = 0; UNITS && q < RT; ++q) scales[q] = scales_ahead[q];
     step(j, std::integral_constant<int, 0>{});
     step(j + 1, std::integral_constant<int, 1>{});
-    if constexpr (D == 4) {
-      step(j + 2, std::integral_constant<int, 2>{});
-      step(j + 3, std::integral_constant<int, 3>{});
-    }
+    step(j + 2, std::integral_constant<int, 2>{});
+    step(j + 3, std::integral_constant<int, 3>{});
     if constexpr (SL == D) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[0][0][k] = x_ahead[0][k];
