@@ -316,17 +316,18 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) 
 
 // The same for up to 16 CB tokens that four wavefronts of different rows share through LDS, 64 RT rows a
 // workgroup: the tokens are read from the L2 once for all of them, KC K-blocks at a time, each chunk while
-// the one before it is worked on.  (16 x 18432 x 7168 in e2m1: 18.5 us; w4_gemv_kernel, whose wavefronts
-// each read all tokens: 33.)
-template <int GP, bool Z, int CB, int RT>
-__global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
+// the one before it is worked on.  KS such groups of four divide K.  (16 x 18432 x 7168 in e2m1: 18.5 us; w4_gemv_kernel,
+// whose wavefronts each read all tokens: 33.  64 tokens, integers: with KS = 2 45 us, with 1 54.)
+template <int GP, bool Z, int CB, int RT, int KS>
+__global__ __launch_bounds__(256 * KS, 2) void w4_batch_kernel(const W4Problem p) {
   constexpr bool E2M1 = GP == 0;
   constexpr int KC = CB <= 2 ? 4 : 2;  // K-blocks a chunk of tokens
   constexpr int PIECES = CB * KC;      // pieces of eight values that a thread brings
   constexpr int XB = KC * 16 * CB * 256;
-  __shared__ __attribute__((aligned(16))) uint8_t xl[2][XB];  // [block][token][16 pieces, piece k at k ^ token % 16]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  extern __shared__ __attribute__((aligned(16))) uint8_t x_lds[]; // [part][2][block][token][16 pieces, piece k at k ^ token % 16]
+  const int tid = threadIdx.x & 255, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), part = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  uint8_t* const xl = x_lds + part * (2 * XB);
   const int c = lane >> 4, r = lane & 15;
   const int all_tiles = (int)((p.N + 15) / 16);
   const int tile = ((int)blockIdx.x * 4 + wave) * RT;
@@ -334,6 +335,7 @@ __global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
   const int T = (int)(p.T - t0 < 16 * CB ? p.T - t0 : 16 * CB);
   const int tiles = all_tiles - tile < 0 ? 0 : all_tiles - tile < RT ? all_tiles - tile : RT;
   const int KB = (int)(p.K / 128), units = (KB + 3) / 4;
+  const int j0 = KB * part / KS, j1 = KB * (part + 1) / KS;  // this part's K-blocks
   const uint32_t s_tile = units * (E2M1 ? 256u : 128u * GP), z_tile = units * 64u * GP;
   const auto rw = shared_run(p.codes + (int64_t)tile * KB * 1024, tiles * KB * 1024u);
   const auto rx = shared_run(p.x + t0 * p.ldx, (uint32_t)(((T - 1) * p.ldx + p.K) * 2));
@@ -348,14 +350,14 @@ __global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
     for (int q = 0; q < RT; ++q) acc[b][q] = v4f{0, 0, 0, 0};
   auto load_w = [&](int j, int i) {
 #pragma unroll
-    for (int q = 0; q < RT; ++q) w[i][q].load(rw, rs, rz, q, j, j < KB ? 0 : kOut, KB, s_tile, z_tile, lane);
+    for (int q = 0; q < RT; ++q) w[i][q].load(rw, rs, rz, q, j, j < j1 ? 0 : kOut, KB, s_tile, z_tile, lane);
   };
   // pieces of a chunk: thread -> (token, K-block, piece), the pieces of a token's chunk side by side
   auto load_x = [&](int j) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int at = i * 256 + tid, t = at / (16 * KC), k = at % (16 * KC);
-      const uint32_t o = t < T && j + k / 16 < KB ? (uint32_t)(t * p.ldx * 2 + j * 256 + k * 16) : kOut;
+      const uint32_t o = t < T && j + k / 16 < j1 ? (uint32_t)(t * p.ldx * 2 + j * 256 + k * 16) : kOut;
       xn[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)o, 0, 0));
     }
   };
@@ -363,14 +365,14 @@ __global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int at = i * 256 + tid, t = at / (16 * KC), k = at % (16 * KC), kb = k / 16, piece = k & 15;
-      *reinterpret_cast<u32x4*>(&xl[buf][((kb * 16 * CB + t) * 16 + (piece ^ (t & 15))) * 16]) = xn[i];
+      *reinterpret_cast<u32x4*>(&xl[buf * XB + ((kb * 16 * CB + t) * 16 + (piece ^ (t & 15))) * 16]) = xn[i];
     }
   };
-  load_x(0);
+  load_x(j0);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < KC; ++i) {
-    load_w(i, i);
+    load_w(j0 + i, i);
     __builtin_amdgcn_sched_barrier(0);
   }
   store_x(0);
@@ -389,7 +391,7 @@ __global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           x[k] = *reinterpret_cast<const bf16x8*>(
-              &xl[buf][((i * 16 * CB + 16 * b + r) * 16 + ((E2M1 ? 4 * c + k : 4 * k + c) ^ r)) * 16]);
+              &xl[buf * XB + ((i * 16 * CB + 16 * b + r) * 16 + ((E2M1 ? 4 * c + k : 4 * k + c) ^ r)) * 16]);
         multiply<GP, Z, RT>(acc[b], x, w[i], v);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -399,7 +401,23 @@ __global__ __launch_bounds__(256, 2) void w4_batch_kernel(const W4Problem p) {
     store_x(buf ^ 1);
     __syncthreads();
   };
-  for (int j = 0, buf = 0; j < KB; j += KC, buf ^= 1) chunk(j, buf);
+  // (every part takes as many turns, a shorter one's last over zeros)
+  const int turns = ((KB + KS - 1) / KS + KC - 1) / KC;
+  for (int i = 0; i < turns; ++i) chunk(j0 + KC * i, i & 1);
+  if constexpr (KS > 1) {
+    // the parts' sums, in order (the tokens are no longer read)
+    v4f* const sums = reinterpret_cast<v4f*>(x_lds);
+    if (part > 0) {
+#pragma unroll
+      for (int i = 0; i < CB * RT; ++i) sums[((part - 1) * 4 + wave) * (64 * CB * RT) + 64 * i + lane] = acc[i / RT][i % RT];
+    }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int s = 0; s < KS - 1; ++s)
+#pragma unroll
+      for (int i = 0; i < CB * RT; ++i) acc[i / RT][i % RT] += sums[(s * 4 + wave) * (64 * CB * RT) + 64 * i + lane];
+  }
 #pragma unroll
   for (int b = 0; b < CB; ++b)
 #pragma unroll
@@ -520,25 +538,33 @@ hipError_t launch_rows(const W4Problem& p, int most, dim3 grid, hipStream_t stre
   return hipGetLastError();
 }
 
+template <int GP, bool Z, int RT>
+hipError_t launch_batch(const W4Problem& p, int most, unsigned chunks, hipStream_t stream) {
+  constexpr int KS = 2;
+  const dim3 grid((unsigned)(((p.N + 15) / 16 + 4 * RT - 1) / (4 * RT)), chunks);
+  const int blocks = (most + 15) / 16;
+  const int lds = KS * 2 * (blocks <= 2 ? 4 : 2) * 16 * blocks * 256;  // two chunks of tokens a part
+  switch (blocks) {
+    case 1: w4_batch_kernel<GP, Z, 1, RT, KS><<<grid, 256 * KS, lds, stream>>>(p); break;
+    case 2: w4_batch_kernel<GP, Z, 2, RT, KS><<<grid, 256 * KS, lds, stream>>>(p); break;
+    case 3: w4_batch_kernel<GP, Z, 3, RT, KS><<<grid, 256 * KS, lds, stream>>>(p); break;
+    default: w4_batch_kernel<GP, Z, 4, RT, KS><<<grid, 256 * KS, lds, stream>>>(p); break;
+  }
+  return hipGetLastError();
+}
+
 // Which kernel.  Up to one tile a compute unit (256), each is a workgroup's, so that all of them work; with more,
 // a wavefront takes two and reads its tokens once for both (1 x 7168 x 18432: 13.2 us against 14.4, 64 x 7168 x
-// 2048: 12.7 against 19.5; at 256 tiles 1 x 4096 x 7168: 7.0 against 5.9).  From 1024 tiles and 5 tokens the rows
-// alone fill the chip with wavefronts that share the tokens through LDS.
+// 2048: 12.7 against 19.5; at 256 tiles 1 x 4096 x 7168: 7.0 against 5.9).  From 5 tokens on, more than 512 tiles fill
+// the chip with wavefronts that share the tokens through LDS, four tiles a workgroup (64 x 10240 x 7168: 33 us against 57;
+// at 448 tiles 41 against 33), and from 1024 on eight (16 x 18432 x 7168: 18.5 against 22).
 template <int GP, bool Z>
 hipError_t launch_gemv(const W4Problem& p, hipStream_t stream) {
   const int64_t tiles = (p.N + 15) / 16;
   const int most = (int)(p.T < 64 ? p.T : 64);
   const unsigned chunks = (unsigned)((p.T + 63) / 64);
-  if (most > 4 && tiles >= 1024) {
-    const dim3 grid((unsigned)((tiles + 7) / 8), chunks);
-    switch ((most + 15) / 16) {
-      case 1: w4_batch_kernel<GP, Z, 1, 2><<<grid, 256, 0, stream>>>(p); break;
-      case 2: w4_batch_kernel<GP, Z, 2, 2><<<grid, 256, 0, stream>>>(p); break;
-      case 3: w4_batch_kernel<GP, Z, 3, 2><<<grid, 256, 0, stream>>>(p); break;
-      default: w4_batch_kernel<GP, Z, 4, 2><<<grid, 256, 0, stream>>>(p); break;
-    }
-    return hipGetLastError();
-  }
+  if (most > 4 && tiles >= 1024) return launch_batch<GP, Z, 2>(p, most, chunks, stream);
+  if (most > 4 && tiles > 512) return launch_batch<GP, Z, 1>(p, most, chunks, stream);
   return tiles <= 256 ? launch_rows<GP, Z, 1>(p, most, dim3((unsigned)tiles, chunks), stream)
                       : launch_rows<GP, Z, 2>(p, most, dim3((unsigned)((tiles + 1) / 2), chunks), stream);
 }

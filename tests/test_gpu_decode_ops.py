@@ -153,7 +153,8 @@ def test_gemv(format, group, zero_points, T, N, K):
 @pytest.mark.parametrize("format,group,zero_points", FORMATS)
 @pytest.mark.parametrize("T,N,K", [(3, 4112, 512), (6, 4113, 1152), (16, 4200, 640), (20, 4099, 512), (40, 4128, 640),
                                    (64, 4111, 384), (4, 16400, 256), (5, 16384, 640), (16, 16401, 384), (17, 16384, 512),
-                                   (33, 16500, 256), (64, 16385, 384), (70, 16384, 128)])
+                                   (33, 16500, 256), (64, 16385, 384), (70, 16384, 128), (5, 8208, 640),
+                                   (16, 8500, 1152), (30, 10001, 256), (48, 8209, 384), (64, 16383, 128), (65, 9000, 1408)])
 def test_gemv_of_many_rows(format, group, zero_points, T, N, K):
     """Two tiles a wavefront, and tokens shared through LDS."""
     test_gemv(format, group, zero_points, T, N, K)
