@@ -13,9 +13,9 @@
 // Operands: v_mfma_f32_16x16x32_bf16 with the weights as the first operand (16 rows) and up
 // to 16 tokens as the second; codes of 8 and 4 bits become bf16 with their power-of-two scale by
 // one conversion for two, without rounding.  (The matrix instruction on e4m3 operands adds its
-// products to about 2^-18 of their magnitudes; a gated activation next to the middle between
-// two codes would go to the other one in some 4 of 10^4 places, against 1 in 10^6 here.  The
-// conversions take a third of the vector units' time at the rate that the weights arrive.)
+// products to about 2^-18 of their magnitudes, and a gated activation next to the middle between
+// two codes went to the other one in 2 of 16384 places of a test, one of them 3% of its token.
+// The conversions run at the full vector rate.)
 // Lane l = 16 c + r holds of a 128-wide K-block of row (or token) r: of e4m3 the columns
 // 16 c .. 16 c + 15 and 64 + 16 c .. + 15, of e2m1 the columns 32 c .. 32 c + 31, eight of
 // them a product; the result holds rows 4 c + i, i < 4, of token r.
@@ -297,7 +297,7 @@ struct Routing {
 // KW-th of K, and share the tokens of it through LDS, where they lie as bf16, a unit of four K-blocks ahead (each wavefront
 // reading them from the L2 by itself: 163 us for 64 tokens; so 145).  With KW = 1 y goes out quantized.  The others are for
 // few experts, where workgroups of 128 columns would leave compute units without work (1 token of 8 experts of 7168 x 2048:
-// 47.2 us, with KW = 2 38.5); y stays in fp32 for moe_down_kernel to quantize, since no workgroup has a whole group.
+// 46.3 us, with KW = 2 38.8; of 2 experts 38.4, 23.7 and with KW = 4 18.0); y stays in fp32 for moe_down_kernel to quantize, since no workgroup has a whole group.
 template <Weights F, bool SMALL, int KW>
 __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
   constexpr int RW = 8 / KW;
@@ -314,11 +314,8 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(const MoeArgs p) {
   routing.open(m, lane, lds, false);
   if (a >= routing.active) return;
   const int e = routing.expert(a, lane);
-  // each wavefront could find the columns, but one does and all read them
-  int n = 0;
-  if (wave == 0) n = routing.columns(e, lane, cols);
+  if (wave == 0) routing.columns(e, lane, cols);
   __syncthreads();
-  (void)n;
   const int KB = m.K / 128, units = (KB + 3) / 4;
   const int u0 = units * part / KW, u1 = units * (part + 1) / KW;
   const int c = lane >> 4, r = lane & 15;

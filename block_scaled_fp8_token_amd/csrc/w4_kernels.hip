@@ -553,11 +553,12 @@ hipError_t launch_batch(const W4Problem& p, int most, unsigned chunks, hipStream
   return hipGetLastError();
 }
 
-// Which kernel.  Up to one tile a compute unit (256), each is a workgroup's, so that all of them work; with more,
-// a wavefront takes two and reads its tokens once for both (1 x 7168 x 18432: 13.2 us against 14.4, 64 x 7168 x
-// 2048: 12.7 against 19.5; at 256 tiles 1 x 4096 x 7168: 7.0 against 5.9).  From 5 tokens on, more than 512 tiles fill
-// the chip with wavefronts that share the tokens through LDS, four tiles a workgroup (64 x 10240 x 7168: 33 us against 57;
-// at 448 tiles 41 against 33), and from 1024 on eight (16 x 18432 x 7168: 18.5 against 22).
+// Which kernel.  Up to one tile a compute unit (256, or with few tokens, which cost little to read twice, 320), each is a
+// workgroup's, so that all of them work; with more, a wavefront takes two and reads its tokens once for both (64 x 7168 x
+// 2048: 13.1 us against 20.2, 1 x 7168 x 18432: 12.6 against 13.0; 1 x 4096 x 7168: 6.8 against 6.1, 5 x 4099 x 7168: 9.9
+// against 8.9).  From 5 tokens on, more than 512 tiles fill the chip with wavefronts that share the tokens through LDS, four
+// tiles a workgroup (64 x 10240 x 7168: 33 us against 57; at 448 tiles 41 against 33), and from 1024 on eight (16 x 18432
+// x 7168: 18.5 against 22).
 template <int GP, bool Z>
 hipError_t launch_gemv(const W4Problem& p, hipStream_t stream) {
   const int64_t tiles = (p.N + 15) / 16;
@@ -565,7 +566,7 @@ hipError_t launch_gemv(const W4Problem& p, hipStream_t stream) {
   const unsigned chunks = (unsigned)((p.T + 63) / 64);
   if (most > 4 && tiles >= 1024) return launch_batch<GP, Z, 2>(p, most, chunks, stream);
   if (most > 4 && tiles > 512) return launch_batch<GP, Z, 1>(p, most, chunks, stream);
-  return tiles <= 256 ? launch_rows<GP, Z, 1>(p, most, dim3((unsigned)tiles, chunks), stream)
+  return tiles <= (most <= 8 ? 320 : 256) ? launch_rows<GP, Z, 1>(p, most, dim3((unsigned)tiles, chunks), stream)
                       : launch_rows<GP, Z, 2>(p, most, dim3((unsigned)((tiles + 1) / 2), chunks), stream);
 }
 

@@ -151,7 +151,7 @@ def test_gemv(format, group, zero_points, T, N, K):
 
 
 @pytest.mark.parametrize("format,group,zero_points", FORMATS)
-@pytest.mark.parametrize("T,N,K", [(3, 4112, 512), (6, 4113, 1152), (16, 4200, 640), (20, 4099, 512), (40, 4128, 640),
+@pytest.mark.parametrize("T,N,K", [(3, 4112, 512), (6, 4113, 1152), (2, 5136, 640), (7, 5137, 512), (8, 5121, 384), (16, 4200, 640), (20, 4099, 512), (40, 4128, 640),
                                    (64, 4111, 384), (4, 16400, 256), (5, 16384, 640), (16, 16401, 384), (17, 16384, 512),
                                    (33, 16500, 256), (64, 16385, 384), (70, 16384, 128), (5, 8208, 640),
                                    (16, 8500, 1152), (30, 10001, 256), (48, 8209, 384), (64, 16383, 128), (65, 9000, 1408)])
