@@ -425,6 +425,31 @@ def test_layer_values_that_are_not_finite(kind):
         w2[3] = kept
 
 
+@pytest.mark.parametrize("T,topk", [(2, 3), (30, 4)])
+def test_layer_weights_of_pairs_left_out_do_not_matter(T, topk):
+    rng = np.random.default_rng(12)
+    layer = Layer(rng, 5, 256, 128, "preshuffled")
+    q, sf = tokens(rng, T, 256)
+    ids = rng.integers(-2, 7, (T, topk)).astype(np.int32)
+    weights = rng.random((T, topk)).astype(np.float32)
+    clean = layer(q, sf, dev(ids), dev(weights))
+    weights[(ids < 0) | (ids >= 5)] = np.nan
+    assert torch.equal(layer(q, sf, dev(ids), dev(weights)), clean) and clean.isfinite().all()
+
+
+@pytest.mark.parametrize("kind", ["plain", "preshuffled"])
+def test_layer_reads_the_exponent_of_block_scales(kind):
+    """As every product of UE8M0 scales: 2^floor(log2 |s|)."""
+    rng = np.random.default_rng(13)
+    layer = Layer(rng, 4, 384, 256, kind)
+    q, sf = tokens(rng, 6, 384)
+    ids, weights = dev(rng.integers(0, 4, (6, 2)).astype(np.int32)), dev(rng.random((6, 2)).astype(np.float32))
+    clean = layer(q, sf, ids, weights)
+    for _, _, s in layer.w:
+        s.mul_(-1.75)
+    assert torch.equal(layer(q, sf, ids, weights), clean)
+
+
 def test_scale_words_past_the_columns_do_not_matter():
     """Bytes of groups past K, and scale words of another token, may hold anything."""
     rng = np.random.default_rng(11)
