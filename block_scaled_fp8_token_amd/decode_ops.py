@@ -9,6 +9,8 @@ outputs that a caller passes must not overlap inputs (not checked).
 """
 from __future__ import annotations
 
+import operator
+
 import torch
 
 from . import _lib, _words
@@ -184,7 +186,9 @@ def w4_group_gemv_nt(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     px, ldx = _rows(x, "x", _BF16, T, K)
     if K % 128 or K == 0:
         raise ValueError("K must be a multiple of 128, got %d" % K)
-    n = int(n)
+    n = operator.index(n)
+    if n < 0:
+        raise ValueError("n must not be negative, got %d" % n)
     tiles, units = (n + 15) // 16, _words(K)
     pc = _whole(codes, "codes", _U8, (tiles, K // 128, 1024))
     pz = None

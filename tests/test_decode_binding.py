@@ -125,6 +125,8 @@ def test_w4_binding():
     refuses(ValueError, "K must", F.w4_group_gemv_nt, z(3, 600), codes, z(2, 2, 16, 4), 20)
     refuses(TypeError, "x:", F.w4_group_gemv_nt, x.float(), codes, z(2, 2, 16, 4), 20)
     refuses(ValueError, "x must", F.w4_group_gemv_nt, z(640, 3).t(), codes, z(2, 2, 16, 4), 20)
+    refuses(ValueError, "n must", F.w4_group_gemv_nt, x, codes[:0], z(0, 2, 16, 4), -5)
+    refuses(TypeError, "integer", F.w4_group_gemv_nt, x, codes, z(2, 2, 16, 4), 20.5)
 
 
 def _layer(name, q=Q, ldq=640, sf=SF, ld_sf=8, ids=I, w=W, w13=W13, s13=S13, w2=W2, s2=S2, base=BASE, ld_base=640, T=5,
