@@ -466,7 +466,8 @@ __global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t* __restric
       word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[6], f[7], scale, 3);
       if (i % lanes == 0) static_cast<uint8_t*>(scales)[i / lanes] = (uint8_t)byte;
     } else {
-      const uint32_t bits = bf16x2_rne(Z ? (hi - lo) / 15.0f : most / 7.0f, 0.0f) & 0xFFFF;
+      // (hi - lo) / 15 by halves, which changes no bit but lets no difference of two finite values pass fp32's range
+      const uint32_t bits = bf16x2_rne(Z ? (0.5f * hi - 0.5f * lo) / 7.5f : most / 7.0f, 0.0f) & 0xFFFF;
       const float scale = bf16_lo(bits);
       float zero = 8.0f;
       if constexpr (Z) zero = scale > 0.0f ? __builtin_fminf(__builtin_rintf(-lo / scale), 15.0f) : 0.0f;

@@ -509,7 +509,7 @@ int moe_decode_layer_w4(const void* q, int64_t ldq, const uint32_t* sf, int64_t 
  *     FP8BS_E2M1: the smallest 2^e with 6 * 2^e >= amax (e >= -126), codes to nearest even.
  *     FP8BS_INT4: s = bf16(amax / 7), c = clamp(rint(w / s) + 8, 0, 15); with zeros s = bf16((max - min) / 15)
  *     over the group's values and 0, z = min(rint(-min / s), 15), c = clamp(rint(w / s) + z, 0, 15), in
- *     fp32; where s is 0, c = z (0 with zeros).
+ *     fp32 (max - min also where it passes fp32's range); where s is 0, c = z (0 with zeros).
  * w4_preshuffle: codes [E][N][K/2], scales and zeros [E][N][K/group] in row order -> the layout that the
  *   products read, rows past N and columns past K zero, with tiles = ceil(N/16), units = ceil(K/512):
  *     codes_out  [E][tiles][K/128][64][16 bytes]   entry 16 c + r of a tile is row r:

@@ -45,6 +45,25 @@ def test_quant_int4(group, zero_points):
         assert np.array_equal(zeros.cpu().numpy(), z)
 
 
+@pytest.mark.parametrize("group", [32, 128])
+def test_quant_of_the_largest_values(group):
+    """A group whose span is past fp32's range: s = bf16(span / 15) with the span in 64 bits."""
+    w = torch.linspace(-1, 1, 128).repeat(3, 1).bfloat16()
+    w[:, ::16], w[:, 15::16] = -1, 1
+    w *= torch.finfo(torch.bfloat16).max
+    codes, scales, zeros = F.w4_group_quant(w.to(DEV), "int4", group, True)
+    s = torch.tensor(2 * torch.finfo(torch.bfloat16).max / 15, dtype=torch.float64).float().bfloat16().item()
+    assert (scales.cpu().float() == s).all()
+    zero = round(torch.finfo(torch.bfloat16).max / s)
+    assert (zeros.cpu() == zero).all()
+    want = (w.double() / s).round().add(zero).clamp(0, 15)
+    # w / s is rounded to fp32 (by at most 8 * 2^-24) before its rounding to an integer, which matters next to a middle
+    # alone: every value is on one, which is exact in fp32, or away from it
+    off = ((w.double() / s) % 1 - 0.5).abs()
+    assert ((off == 0) | (off > 2.0 ** -20)).all()
+    assert np.array_equal(R.nibbles(codes.cpu().numpy()), want.numpy())
+
+
 def test_quant_e2m1():
     rng = np.random.default_rng(1)
     w = bf16(rng, 2, 40, 384, std=0.05)
