@@ -31,7 +31,8 @@ def _moe(name, q, sf, topk_ids, weights, w13, s13, w2, s2, H, shapes, dtypes, ba
     T, K = _2d(q, "q")
     topk = _2d(topk_ids, "topk_ids")[1]
     if T > 64:
-        raise ValueError("q: %d tokens; the layer takes at most 64, larger batches go through the masked GEMMs" % T)
+        raise ValueError("q: %d tokens; the layer takes at most 64, larger batches go %s"
+                         % (T, "in pieces" if name == "moe_decode_layer_w4" else "through the masked GEMMs"))
     pq, ldq = _rows(q, "q", _E4M3, T, K)
     _typed(sf, "sf", _U32)
     if sf.dim() != 2 or sf.shape[0] != _words(K) or sf.shape[1] < T or sf.stride(1) != 1 or (
@@ -91,7 +92,8 @@ def moe_decode_layer_w4(q: torch.Tensor, sf: torch.Tensor, topk_ids: torch.Tenso
                         w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor,
                         base: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """moe_decode_layer on e2m1 weights as w4_preshuffle lays them out: w13 uint8 [E, 2H/16, K/128, 1024] with s13
-    uint8 [E, 2H/16, ceil(K/512), 64, 4], w2 [E, K/16, H/128, 1024] with s2 [E, K/16, ceil(H/512), 64, 4]."""
+    uint8 [E, 2H/16, ceil(K/512), 64, 4], w2 [E, K/16, H/128, 1024] with s2 [E, K/16, ceil(H/512), 64, 4].
+    The masked GEMMs take no such weights: more than 64 tokens go in pieces of 64, each of which reads its experts again."""
     if stream is not None:
         return _on_stream(stream, moe_decode_layer_w4, q, sf, topk_ids, weights, w13, s13, w2, s2, base, out)
     if w13.dim() != 4 or w2.dim() != 4 or w13.shape[1] % 16:

@@ -478,7 +478,9 @@ int silu_mul_backward_from_checkpoint(const void* d_y, const int32_t* masked_m, 
  *              call uses until this one's work on the stream is done
  *   K % 128 == 0 and H % 128 == 0, both at most 65536; the rows of q and of sf span less than 2 GiB.
  * moe_decode_layer_preshuffled takes w13 and w2 in the layout of fp8_weight_preshuffle (rows = 2H
- * and K of each expert), moe_decode_layer_w4 in e2m1 as w4_preshuffle lays them out.
+ * and K of each expert), moe_decode_layer_w4 in e2m1 as w4_preshuffle lays them out.  More than
+ * 64 tokens go through the masked GEMMs; those take no e2m1 weights, so on these they go in
+ * pieces of 64, each of which reads its experts again.
  * Equal calls give equal bits.
  */
 int64_t moe_decode_layer_scratch_bytes(int64_t T, int32_t topk, int64_t H);

@@ -81,6 +81,14 @@ def test_layer_binding(kind):
     bad(ValueError, "device", out=z(T, K, dtype=bf).to("meta"))
 
 
+@pytest.mark.parametrize("kind,way", [("plain", "masked GEMMs"), ("preshuffled", "masked GEMMs"), ("w4", "in pieces")])
+def test_layer_names_a_way_for_larger_batches(kind, way):
+    """One that exists: the masked GEMMs take no e2m1 weights."""
+    with pytest.raises(ValueError, match=way) as refusal:
+        CALLS[kind](**{**layer_args(kind), "q": z(65, K, dtype=u8)})
+    assert ("masked" in str(refusal.value)) == (kind != "w4")
+
+
 def test_w4_binding():
     passes_checks(F.w4_group_quant, z(5, 256))
     passes_checks(F.w4_group_quant, z(2, 5, 256), "int4", 32, True)
