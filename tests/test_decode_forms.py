@@ -41,13 +41,20 @@ def layer(kind, T, topk, E, K, H):
     return "layer %s %d %d %d %d %d" % (kind, T, topk, E, K, H)
 
 
+def product(format, T, N, K):
+    return "product %d %d %d %s %d %d" % (T, N, K, *format)
+
+
 LAYER = ("moe_gate_up_kernel", "moe_down_kernel")
+PRODUCT = ("w4_gemv_kernel", "w4_batch_kernel")
 
 
 @pytest.mark.parametrize("names,lines", [
     (LAYER, [layer(kind, T, topk, E, K, H) for kind in ops.KINDS
              for T, E, topk, K, H, _ in sizes(ops.test_layer, forms.test_layer)]),
-], ids=["layer-values"])
+    (PRODUCT, [product(format, *size) for format in ops.FORMATS
+               for size in sizes(ops.test_gemv, ops.test_gemv_of_many_rows, forms.test_gemv)]),
+], ids=["layer-values", "product-values"])
 def test_no_kernel_is_left_out(kernels_of, names, lines):
     have = {k for k in kernels_of(["kernels"]) if any(n in k for n in names)}
     missing = have - kernels_of(lines)
