@@ -1,4 +1,4 @@
-"""No kernel of the decode step's operators is without a test of its values: the sizes of the
+"""No kernel of the decode step's operators is without a test of its values and of the ways of calling it: the sizes of the
 GPU tests, put through the library's own choice of kernels (tests/decode_forms.cpp, which stands in for the HIP runtime;
 nothing runs on a GPU)."""
 import os
@@ -52,10 +52,21 @@ PRODUCT = ("w4_gemv_kernel", "w4_batch_kernel")
 @pytest.mark.parametrize("names,lines", [
     (LAYER, [layer(kind, T, topk, E, K, H) for kind in ops.KINDS
              for T, E, topk, K, H, _ in sizes(ops.test_layer, forms.test_layer)]),
+    (LAYER, [layer(kind, *size) for kind in ops.KINDS for size in forms.LAYER_FORMS]),
     (PRODUCT, [product(format, *size) for format in ops.FORMATS
                for size in sizes(ops.test_gemv, ops.test_gemv_of_many_rows, forms.test_gemv)]),
-], ids=["layer-values", "product-values"])
+], ids=["layer-values", "layer-calls", "product-values"])
 def test_no_kernel_is_left_out(kernels_of, names, lines):
     have = {k for k in kernels_of(["kernels"]) if any(n in k for n in names)}
     missing = have - kernels_of(lines)
     assert have and not missing, "\n".join(sorted(missing))
+
+
+def test_every_form_of_a_product_is_called(kernels_of):
+    """Each choice of tiles and tokens, in one format at least."""
+    def form(kernel):
+        head, args = kernel.split("<", 1)
+        return head.split("::")[-1], args.split(",", 2)[2]
+    have = {form(k) for k in kernels_of(["kernels"]) if any(n in k for n in PRODUCT)}
+    lines = [product(ops.FORMATS[i % len(ops.FORMATS)], T, N, 640) for i, (T, N) in enumerate(forms.GEMV_FORMS)]
+    assert have == {form(k) for k in kernels_of(lines)}

@@ -1,12 +1,13 @@
-"""The operators of a decode step in every form that their sizes choose: values against references in 64 bits and values that
-are not finite (tests/test_decode_forms.py checks that no kernel is left out)."""
+"""The operators of a decode step in every form that their sizes choose: values against references in 64 bits, values that
+are not finite, and the ways of calling them (tests/test_decode_forms.py checks that no kernel is left out)."""
 import numpy as np
 import pytest
 import torch
 
 import block_scaled_fp8_token_amd as F
+import test_gpu_decode_calls as calls
 import test_gpu_decode_ops as ops
-from test_gpu_decode_ops import DEV, FORMATS, KINDS, bf16, weights_of
+from test_gpu_decode_ops import DEV, FORMATS, KINDS, Layer, bf16, dev, tokens, weights_of
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,74 @@ def test_gemv_values_that_are_not_finite_stay_with_their_token(format, group, ze
     same = [t for t in range(T) if t not in (1, T - 1)]
     assert clean.isfinite().all() and torch.equal(got[same], clean[same])
     assert got[1].isnan().all() and not got[T - 1].isfinite().any()
+
+
+#: tokens, choices, experts, hidden and half size of a layer in each form: K in four parts and in two; then up to 64 pairs
+#: and more, by 16, 32 and 64 tokens, with 16 and with 32 output columns a workgroup
+LAYER_FORMS = [(1, 2, 6, 512, 256), (1, 48, 48, 256, 256)] + [
+    (T, topk, 4, K, H) for K in (512, 4224) for T, topk, H in (
+        (16, 4, 640), (20, 3, 128), (40, 1, 128), (16, 5, 128), (24, 4, 128), (40, 3, 128))]
+#: a product in each form of tiles and tokens
+GEMV_FORMS = [(1, 100), (7, 300), (14, 100), (20, 100), (40, 100), (64, 100), (3, 5200), (6, 5200), (14, 4200), (20, 4200),
+              (40, 4200), (64, 4200), (6, 9000), (20, 9000), (40, 9000), (64, 9000), (6, 16400), (20, 16400), (40, 16400),
+              (64, 16400)]
+
+
+def layers(rng, kind):
+    out = []
+    for T, topk, E, K, H in LAYER_FORMS:
+        layer = Layer(rng, E, K, H, kind)
+        q, sf = tokens(rng, T, K)
+        ids, w = dev(rng.integers(0, E, (T, topk)).astype(np.int32)), dev(rng.random((T, topk)).astype(np.float32))
+        base = bf16(rng, T, K).to(DEV)
+        out.append((lambda o, a=(layer, q, sf, ids, w, base), **kw: a[0](*a[1:], out=o, **kw), (T, K)))
+    return out
+
+
+def products(rng, kind):
+    out = []
+    for i, (T, N) in enumerate(GEMV_FORMS):
+        _, _, laid = weights_of(rng, N, 640, *FORMATS[i % len(FORMATS)])
+        x = bf16(rng, T, 640).to(DEV)
+        out.append((lambda o, a=(x, laid, N), **kw: F.w4_group_gemv_nt(a[0], a[1][0], a[1][1], a[2], zeros=a[1][2], out=o, **kw),
+                    (T, N)))
+    return out
+
+
+@pytest.mark.parametrize("way", ["test_named_streams", "test_calls_beside_each_other", "test_captured_and_replayed"])
+@pytest.mark.parametrize("kind", KINDS + ["products"])
+def test_ways_of_calling(monkeypatch, kind, way):
+    monkeypatch.setattr(calls, "works", lambda rng: (products if kind == "products" else layers)(rng, kind))
+    getattr(calls, way)()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_experts_past_32_bits(kind):
+    """The last experts of weights past 2^31 bytes, against a copy of them that has as many experts as the call has pairs: the
+    same kernels with the same order of sums, so equal bits."""
+    T, topk, K, H = 3, 2, 7168, 2048
+    pairs = T * topk
+    E = 220 if kind == "w4" else 120
+    rng = np.random.default_rng(15)
+    q, sf = tokens(rng, T, K)
+    g = torch.Generator(device=DEV).manual_seed(3)
+
+    def codes(*shape):  # finite e4m3, or any e2m1
+        c = torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.uint8)
+        return c if kind == "w4" else c & 0xF7
+    if kind == "w4":
+        w13, w2 = codes(E, 2 * H // 16, K // 128, 1024), codes(E, K // 16, H // 128, 1024)
+        s13, s2 = (torch.full(s, 117, dtype=torch.uint8, device=DEV) for s in ((E, 2 * H // 16, 14, 64, 4), (E, K // 16, 4, 64, 4)))
+    else:
+        w13, w2 = codes(E, 2 * H, K), codes(E, K, H)
+        s13, s2 = (torch.full(s, 2.0 ** -13, device=DEV) for s in ((E, 2 * H // 128, K // 128), (E, K // 128, H // 128)))
+    assert w13.numel() > 1 << 31
+    ids = dev(np.stack([E - pairs + rng.permutation(pairs)[:topk] for _ in range(T)]).astype(np.int32))
+    ids[0, 0] = E - 1
+    w = torch.rand(T, topk, generator=g, device=DEV)
+    call = getattr(F, ops.CALL[kind])
+    got = call(q, sf, ids, w, w13, s13, w2, s2)
+    want = call(q, sf, ids - (E - pairs), w, *(t[-pairs:].contiguous() for t in (w13, s13, w2, s2)))
+    assert got.isfinite().all() and got.abs().max() > 0 and torch.equal(got, want)
+    del w13, w2
+    torch.cuda.empty_cache()
