@@ -469,6 +469,9 @@ int silu_mul_backward_from_checkpoint(const void* d_y, const int32_t* masked_m, 
  * token may name an expert twice.  It is what the dispatch quantization, the masked products,
  * silu_mul_quant_group_pack and moe_combine compute, without their roundings of the products
  * to bf16.  Values that are not finite stay with their token.
+ * The products take the values v in bf16, which holds them exactly under block scales and scale
+ * bytes of 2^-124 to 2^119 (e2m1: bytes 1 to 252); past those, values of 2^128 and more are
+ * infinite, and what of a value is under 2^-133 is lost.
  *   q        : e4m3 [T][ldq], 1 <= T <= 64;  sf : uint32 [ceil(K/512)][ld_sf], ld_sf >= T
  *   topk_ids : int32 [T][topk];  weights : fp32 [T][topk];  1 <= topk <= 64
  *   w13, s13 : e4m3 [E][2H][K], fp32 [E][2H/128][K/128];  w2, s2 : e4m3 [E][K][H], fp32
@@ -501,14 +504,16 @@ int moe_decode_layer_w4(const void* q, int64_t ldq, const uint32_t* sf, int64_t 
 /*
  * Weights of 4 bits under group scales.  Two formats:
  *   FP8BS_E2M1  codes of 1 + 2 + 1 bits (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), a UE8M0
- *               byte b for every 32 columns: value = code * 2^(b - 127), b from 1 to 254
+ *               byte b for every 32 columns: value = code * 2^(b - 127), b from 1 to 254; values of
+ *               2^128 and more (codes from 4 on with b = 253, from 2 on with 254) are infinite
  *   FP8BS_INT4  codes c = 0..15, a bf16 scale s for every 32, 64 or 128 columns, and a zero point z
  *               (uint8) beside it, or 8 without one: value = s * (c - z)
  * K % 128 == 0, K <= 65536.
  *
  * w4_group_quant: bf16 w [rows][K] (contiguous, finite) -> codes [rows][K/2] (even column in the low
  *   half of a byte), scales [rows][K/group], zeros [rows][K/group] or NULL (FP8BS_INT4 only).
- *     FP8BS_E2M1: the smallest 2^e with 6 * 2^e >= amax (e >= -126), codes to nearest even.
+ *     FP8BS_E2M1: the smallest 2^e with 6 * 2^e >= amax (e >= -126), codes to nearest even (a w from
+ *     3.5 * 2^126 on is rounded to 2^128, which is infinite as above).
  *     FP8BS_INT4: s = bf16(amax / 7), c = clamp(rint(w / s) + 8, 0, 15); with zeros s = bf16((max - min) / 15)
  *     over the group's values and 0, z = min(rint(-min / s), 15), c = clamp(rint(w / s) + z, 0, 15), in
  *     fp32 (max - min also where it passes fp32's range); where s is 0, c = z (0 with zeros).

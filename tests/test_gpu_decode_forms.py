@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import block_scaled_fp8_token_amd as F
+import decode_reference as R
 import test_gpu_decode_calls as calls
 import test_gpu_decode_ops as ops
 from test_gpu_decode_ops import DEV, FORMATS, KINDS, Layer, bf16, dev, tokens, weights_of
@@ -58,6 +59,66 @@ def test_gemv_values_that_are_not_finite_stay_with_their_token(format, group, ze
     same = [t for t in range(T) if t not in (1, T - 1)]
     assert clean.isfinite().all() and torch.equal(got[same], clean[same])
     assert got[1].isnan().all() and not got[T - 1].isfinite().any()
+
+
+@pytest.mark.parametrize("T,N", [(1, 16), (6, 5152), (20, 32), (20, 8224), (6, 16400)])
+@pytest.mark.parametrize("byte,most", [(1, 7), (2, 7), (251, 7), (252, 7), (253, 5), (254, 3)])
+def test_gemv_e2m1_scales_at_their_ends(byte, most, T, N):
+    """Every code whose value is under 2^128, a code a row: sums of one power of two are exact."""
+    K = 128
+    codes = np.resize(np.concatenate([np.arange(most + 1), 8 + np.arange(most + 1)]), N).astype(np.uint8)
+    laid = F.w4_preshuffle(dev(np.repeat(17 * codes[:, None], K // 2, 1)), dev(np.full((N, K // 32), byte, np.uint8)))
+    e = max(-120, min(120, 127 - byte))
+    got = F.w4_group_gemv_nt(torch.full((T, K), 2.0 ** e, dtype=torch.bfloat16, device=DEV), laid[0], laid[1], N)
+    want = K * R.E2M1[codes] * 2.0 ** (e + byte - 127)
+    assert (got.double().cpu().numpy() == want).all()
+
+
+def e4m3_code(value):
+    return torch.tensor(value).to(torch.float8_e4m3fn).view(torch.uint8).item()
+
+
+@pytest.mark.parametrize("T", [1, 20, 40])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("where", ["up", "down", "tokens"])
+@pytest.mark.parametrize("end", ["low", "high"])
+def test_layer_scales_at_their_ends(where, end, kind, T):
+    """One product of powers of two a column, so that the layer's output is exact: gate 32 (its silu in fp32 is 32), up and
+    down one weight each, under the smallest and largest scales that bf16 holds every code of."""
+    K = H = 128
+    w4 = kind == "w4"
+    lo, hi = (-126, 125) if w4 and where != "tokens" else (-124, 119)
+    codes = [0.5, 1.0, 6.0] if w4 and where != "tokens" else [2.0 ** -9, 1.0, 448.0]
+    s = lo if end == "low" else hi
+    # exponents of the scales of the tokens, the gate's weights (their code is 1), the up product's and the down product's
+    t = {"up": max(-100, min(100, -s)), "down": 0, "tokens": s}[where]
+    gate = 5 - 8 - t  # the tokens' code for the gate is 256
+    up = {"up": s, "down": -30 if s > 0 else 0, "tokens": max(-100, min(100, -s))}[where]
+    down = s if where == "down" else 0
+    for code in codes:
+        u, d, x = (code if where == n else 1.0 for n in ("up", "down", "tokens"))
+        q = torch.zeros(T, K, dtype=torch.uint8, device=DEV)
+        q[:, 0], q[:, 1] = e4m3_code(256.0), e4m3_code(x)
+        sf = torch.full((1, T), 127 + t, dtype=torch.int32, device=DEV)
+        w13, w2 = np.zeros((1, 2 * H, K)), np.zeros((1, K, H))
+        w13[:, :H, 0], w13[:, H:, 1], w2[:, :, 0] = 1.0, u, d
+        e13 = np.repeat(np.array([gate, up]), H)
+        if w4:
+            def four(w, e):
+                n = np.abs(w[..., None] - R.E2M1[:8]).argmin(-1)
+                b = np.repeat((127 + e).astype(np.uint8)[None, :, None], w.shape[2] // 32, 2)
+                return F.w4_preshuffle(dev(R.packed(n)), dev(b))[:2]
+            args = *four(w13, e13), *four(w2, np.full(K, down))
+        else:
+            def eight(w):
+                c = torch.from_numpy(w).float().to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+                return c if kind == "plain" else torch.stack([F.fp8_weight_preshuffle(c[0])])
+            args = (eight(w13), torch.tensor([[[2.0 ** gate], [2.0 ** up]]], device=DEV), eight(w2),
+                    torch.full((1, 1, 1), 2.0 ** down, device=DEV))
+        got = getattr(F, ops.CALL[kind])(q, sf, torch.zeros(T, 1, dtype=torch.int32, device=DEV),
+                                         torch.ones(T, 1, device=DEV), *args)
+        want = 32.0 * u * x * 2.0 ** (t + up) * d * 2.0 ** down
+        assert (got.double() == want).all(), (code, want, got[0, :2])
 
 
 #: tokens, choices, experts, hidden and half size of a layer in each form: K in four parts and in two; then up to 64 pairs
