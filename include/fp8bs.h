@@ -526,8 +526,8 @@ int moe_decode_layer_w4(const void* q, int64_t ldq, const uint32_t* sf, int64_t 
  *       4 b + c of row r;  FP8BS_INT4  [E][tiles][units][16][512/group]
  * w4_group_gemv_nt: out[t][n] = bf16( sum over k of x[t][k] * w[n][k] ), w in that layout (E = 1), sums in
  *   fp32.  Made for few rows of x: every 64 of them read the weights once.  zeros may be NULL.  A value of x that
- *   is not finite, or (FP8BS_INT4, whose codes are taken as 16 + c first) whose 32-fold sums pass fp32's range, makes
- *   its own row not finite, and no other.
+ *   is not finite, or (FP8BS_INT4, whose codes are taken as 16 + c first) whose 32-fold sums, or z-fold ones if a zero
+ *   point is larger, pass fp32's range, makes its own row not finite, and no other.
  *   x : bf16 [T][ldx];  out : bf16 [T][ld_out], ld_out >= N, rows 2-byte aligned;  T <= 2^21, N <= 2^27,
  *   64 rows of x span less than 2 GiB.
  */

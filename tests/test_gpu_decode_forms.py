@@ -74,6 +74,21 @@ def test_gemv_e2m1_scales_at_their_ends(byte, most, T, N):
     assert (got.double().cpu().numpy() == want).all()
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N", [(1, 64), (7, 5137), (20, 48), (40, 4128), (20, 8208)])
+def test_gemv_zero_points_of_a_byte(group, T, N):
+    """Zero points up to 255, in sums that fp32 holds exactly: 640 * 4 * 255 of tokens up to 4, under scales of 1/2 to 4."""
+    rng = np.random.default_rng([T, N, group])
+    K = 640
+    codes, zeros = rng.integers(0, 256, (N, K // 2), np.uint8), rng.integers(0, 256, (N, K // group)).astype(np.uint8)
+    sv = np.exp2(rng.integers(-1, 3, (N, K // group))).astype(np.float64)
+    laid = F.w4_preshuffle(dev(codes), R.round_bf16(sv).to(DEV), dev(zeros))
+    x = torch.from_numpy(rng.integers(-4, 5, (T, K)).astype(np.float32)).to(torch.bfloat16)
+    got = F.w4_group_gemv_nt(x.to(DEV), laid[0], laid[1], N, zeros=laid[2])
+    want = R.round_bf16(R.bf16_values(x) @ R.w4_values(codes, sv, zeros).T)
+    assert torch.equal(got.cpu().view(torch.int16), want.view(torch.int16))
+
+
 def e4m3_code(value):
     return torch.tensor(value).to(torch.float8_e4m3fn).view(torch.uint8).item()
 
