@@ -7,8 +7,8 @@
 // Every weight of an expert that some token has chosen is read once and used for all its
 // tokens; with at most 64 tokens that reading is what the layer costs, so both kernels
 // are built to keep it going: a wavefront owns 16 or 32 rows of a weight matrix, each lane
-// loads its operand's bytes straight into registers four K-blocks ahead (streaming loads),
-// and the few bytes of the tokens come from LDS or the L2.
+// loads its operand's bytes straight into registers four K-blocks ahead (streaming loads,
+// but cached ones of plain rows), and the few bytes of the tokens come from LDS or the L2.
 //
 // Operands: v_mfma_f32_16x16x32_bf16 with the weights as the first operand (16 rows) and up
 // to 16 tokens as the second; codes of 8 and 4 bits become bf16 with their power-of-two scale by

@@ -3,8 +3,8 @@
 //
 // The layout.  Codes lie in tiles of 16 rows by 128 columns, 1 KB each, that a wavefront
 // loads with one 16-byte instruction: lane 16 c + r holds row r,
-//   e2m1      columns 32 c .. 32 c + 31 in order (one scale, and the operand of the scaled
-//             matrix instruction as it is)
+//   e2m1      columns 32 c .. 32 c + 31 in order (one scale; a word is the eight columns of
+//             one operand once they are bf16)
 //   integers  in word i the columns 32 i + 8 c + 0, 2, 4, 6, 1, 3, 5, 7 (so the same word of
 //             every lane lies in one group, and one shift and mask give two neighbours)
 // Scales lie in units of 512 columns: e2m1 [tile][unit][lane][4 blocks], integers
@@ -316,8 +316,8 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_gemv_kernel(const W4Problem p) 
 
 // The same for up to 16 CB tokens that four wavefronts of different rows share through LDS, 64 RT rows a
 // workgroup: the tokens are read from the L2 once for all of them, KC K-blocks at a time, each chunk while
-// the one before it is worked on.  KS such groups of four divide K.  (16 x 18432 x 7168 in e2m1: 18.5 us; w4_gemv_kernel,
-// whose wavefronts each read all tokens: 33.  64 tokens, integers: with KS = 2 45 us, with 1 54.)
+// the one before it is worked on.  KS such groups of four divide K.  (16 x 18432 x 7168 in e2m1: 18.7 us; w4_gemv_kernel,
+// whose wavefronts each read all tokens: 30.  64 tokens, integers: with KS = 2 45 us, with 1 54.)
 template <int GP, bool Z, int CB, int RT, int KS>
 __global__ __launch_bounds__(256 * KS, 2) void w4_batch_kernel(const W4Problem p) {
   constexpr bool E2M1 = GP == 0;
@@ -555,11 +555,23 @@ hipError_t launch_batch(const W4Problem& p, int most, unsigned chunks, hipStream
 }
 
 // Which kernel.  Up to one tile a compute unit (256, or with few tokens, which cost little to read twice, 320), each is a
-// workgroup's, so that all of them work; with more, a wavefront takes two and reads its tokens once for both (64 x 7168 x
-// 2048: 13.1 us against 20.2, 1 x 7168 x 18432: 12.6 against 13.0; 1 x 4096 x 7168: 6.8 against 6.1, 5 x 4099 x 7168: 9.9
-// against 8.9).  From 5 tokens on, more than 512 tiles fill the chip with wavefronts that share the tokens through LDS, four
-// tiles a workgroup (64 x 10240 x 7168: 33 us against 57; at 448 tiles 41 against 33), and from 1024 on eight (16 x 18432
-// x 7168: 18.5 against 22).
+// workgroup's, so that all of them work; with more, a wavefront takes two and reads its tokens once for both.  From 5 tokens
+// on, more than 512 tiles fill the chip with wavefronts that share the tokens through LDS, four tiles a workgroup, and from
+// 1024 on eight.  Both sides, in us with K = 7168 where it is not named:
+//   one tile a workgroup, two (1 token, int4 of 128)       257 tiles 6.1, 7.0   320: 6.7, 6.9   448: 7.0, 7.2 (of K = 18432
+//                                                          12.9, 12.6)
+//   (5 tokens, int4 of 32 with zero points; int4 of 128)   257 tiles 8.7, 9.5; 8.0, 7.7         320: 9.9, 9.7; 9.0, 7.7
+//   (8 tokens, the same)                                   257 tiles 10.5, 9.8; 9.7, 8.4        320: 11.7, 10.0; 10.8, 8.5
+//   (9 tokens, int4 of 128)                                200 tiles 7.7, 8.8   257: 11.3, 8.9
+//   (64 tokens, int4 of 128 with zero points)              448 tiles, K = 2048: 19.7, 12.8
+//   two tiles a workgroup, four through LDS (int4 of 128; e2m1)
+//                    5 tokens   512 tiles 8.2, 13.2; 8.1, 11.3     576: 11.7, 13.0; 12.1, 11.3    960: 12.6, 14.0; 13.0, 12.5
+//                   16 tokens   512 tiles 11.5, 13.5; 12.2, 12.0   576: 18.7, 13.7; 20.4, 12.2    960: 19.5, 14.3; 21.2, 13.4
+//                   64 tokens   512 tiles 30.9, 32.4; 32.2, 27.0   576: 57.4, 32.6; 61.3, 27.2    960: 58.2, 34.4; 62.9, 29.1
+//   four tiles through LDS, eight (16 tokens)              1024 tiles, int4 of 128: 14.6, 19.0    1152, e2m1: 22.6, 18.7
+// So the ends are not the best for all: 320 costs up to 3 us with 5 to 8 tokens, except with zero points of small groups
+// near 257 tiles; sharing the tokens of 5 costs 1.4 with integers, and 64 of e2m1 would gain by it from fewer tiles on (448
+// of K = 18432: 75.8, 61.7); at 1024 tiles, which are one workgroup of four tiles for each compute unit, eight tiles cost 4 to 11.
 template <int GP, bool Z>
 hipError_t launch_gemv(const W4Problem& p, hipStream_t stream) {
   const int64_t tiles = (p.N + 15) / 16;
