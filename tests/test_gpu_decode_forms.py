@@ -205,3 +205,81 @@ def test_experts_past_32_bits(kind):
     assert got.isfinite().all() and got.abs().max() > 0 and torch.equal(got, want)
     del w13, w2
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,E,topk,K,H,base", [(1, 1, 1, 65536, 128, True), (20, 1, 1, 65536, 128, False),
+                                               (3, 1, 1, 128, 65536, False), (33, 1, 2, 128, 65536, True)])
+def test_layer_of_the_largest_sizes(kind, T, E, topk, K, H, base):
+    rng = np.random.default_rng([T, K])
+    layer = Layer(rng, E, K, H, kind)
+    q, sf = tokens(rng, T, K)
+    ids, weights = np.zeros((T, topk), np.int32), dev(rng.random((T, topk)).astype(np.float32))
+    ids[:, 1:] = -1
+    args = (q, sf, dev(ids), weights, bf16(rng, T, K).to(DEV) if base else None)
+    ops.check_layer(layer, layer(*args), args)
+
+
+@pytest.mark.parametrize("format,group,zero_points", FORMATS)
+@pytest.mark.parametrize("T,N,K", [(2, 20, 65536), (20, 16, 65536), (64, 16, 65536)])
+def test_gemv_of_the_largest_k(format, group, zero_points, T, N, K):
+    ops.test_gemv(format, group, zero_points, T, N, K)
+
+
+@pytest.mark.parametrize("T,N", [(6, 8208), (40, 16400)])
+def test_gemv_through_lds_of_the_largest_k(T, N):
+    """Against the same rows of weights in a product of few, in sums that are exact: under 2 * 32 * 65536 = 2^22."""
+    K = 65536
+    g = torch.Generator(device=DEV).manual_seed(4)
+    codes = torch.randint(0, 256, (-(-N // 16), K // 128, 1024), generator=g, device=DEV, dtype=torch.uint8)
+    scales = torch.ones(-(-N // 16), K // 512, 16, 4, dtype=torch.bfloat16, device=DEV)
+    x = torch.randint(-2, 3, (T, K), generator=g, device=DEV).to(torch.bfloat16)
+    got = F.w4_group_gemv_nt(x, codes, scales, N)
+    for at in (0, 200, N // 16 - 4):
+        want = F.w4_group_gemv_nt(x, codes[at:at + 4].contiguous(), scales[at:at + 4].contiguous(), 64)
+        assert torch.equal(got[:, 16 * at:16 * at + 64], want)
+    del codes
+    torch.cuda.empty_cache()
+
+
+def far_apart(t, ld):
+    """t's rows, ld elements from one to the next."""
+    wide = torch.empty(t.shape[0] * ld, dtype=t.dtype, device=DEV).view(t.shape[0], ld)[:, :t.shape[1]]
+    wide.copy_(t)
+    return wide
+
+
+@pytest.mark.parametrize("T,topk", [(64, 2), (33, 1), (3, 2)])
+def test_layer_of_rows_far_apart(T, topk):
+    """Rows of q and of the scale words that span nearly 2 GiB, as far as the layer takes them, and rows of base and out past
+    2^32 elements."""
+    rng = np.random.default_rng(T)
+    K = 640
+    layer = Layer(rng, 4, K, 256, "plain")
+    q, sf = tokens(rng, T, K)
+    ids, w = dev(rng.integers(0, 4, (T, topk)).astype(np.int32)), dev(rng.random((T, topk)).astype(np.float32))
+    base = bf16(rng, T, K).to(DEV)
+    want = layer(q, sf, ids, w, base=base)
+    ldq = ((1 << 31) // T - K) // 16 * 16
+    ld = ((1 << 32) // (T - 1) // 8 + 1) * 8
+    out = far_apart(torch.zeros(T, K, dtype=torch.bfloat16, device=DEV), ld)
+    got = layer(far_apart(q, ldq), far_apart(sf[:, :T], (1 << 29) - 128), ids, w, base=far_apart(base, ld), out=out)
+    assert got is out and torch.equal(got, want)
+    del got, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,N", [(3, 100), (64, 100), (40, 8208), (130, 100)])
+def test_gemv_of_rows_far_apart(T, N):
+    """64 rows of x that span nearly 2 GiB, and rows of out past 2^32 elements."""
+    rng = np.random.default_rng(T)
+    K = 640
+    _, _, laid = weights_of(rng, N, K, "int4", 64, True)
+    x = bf16(rng, T, K).to(DEV)
+    want = F.w4_group_gemv_nt(x, laid[0], laid[1], N, zeros=laid[2])
+    ldx = ((1 << 30) // min(T, 64) - K) // 8 * 8
+    out = far_apart(torch.zeros(T, N, dtype=torch.bfloat16, device=DEV), (1 << 32) // (T - 1) + N)
+    got = F.w4_group_gemv_nt(far_apart(x, ldx), laid[0], laid[1], N, zeros=laid[2], out=out)
+    assert got is out and torch.equal(got, want)
+    del got, out
+    torch.cuda.empty_cache()
