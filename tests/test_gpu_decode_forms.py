@@ -283,3 +283,56 @@ def test_gemv_of_rows_far_apart(T, N):
     assert got is out and torch.equal(got, want)
     del got, out
     torch.cuda.empty_cache()
+
+
+def made(w, format, group, zero_points, **kw):
+    """w in 4 bits, in row order and laid out."""
+    rows = F.w4_group_quant(w, format, group, zero_points, **kw)
+    return [t for t in (*rows, *F.w4_preshuffle(*rows, **kw)) if t is not None]
+
+
+@pytest.mark.parametrize("format,group,zero_points", [("e2m1", 32, False), ("int4", 64, True)])
+def test_weights_past_32_bits(format, group, zero_points):
+    """Past 2^32 values: the first and the last matrix against the same alone."""
+    E, N, K = 520, 4096, 2048
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    some = torch.randn(4, N, K, generator=g, device=DEV).to(torch.bfloat16)
+    for e in range(E):
+        w[e] = some[e % 4]
+    assert w.numel() > 1 << 32
+    got = made(w, format, group, zero_points)
+    for e in (0, E // 2, E - 1):
+        for a, b in zip(got, made(w[e:e + 1], format, group, zero_points)):
+            assert torch.equal(a[e], b[0])
+    del w, got
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("format,group,zero_points", [("e2m1", 32, False), ("int4", 128, False), ("int4", 32, True)])
+def test_weights_on_streams_and_in_graphs(format, group, zero_points):
+    rng = np.random.default_rng(16)
+    ws = [bf16(rng, 3, 50, 1152, std=0.05).to(DEV) for _ in range(2)]
+    wants = [made(w, format, group, zero_points) for w in ws]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ws]
+    for _ in range(4):
+        got = []
+        for w, s in zip(ws, streams):
+            got.append(made(w, format, group, zero_points, stream=s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, wants) for a, b in zip(g, w))
+    w = ws[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = made(w, format, group, zero_points)
+    for turn in range(4):
+        w.copy_(ws[turn % 2])
+        for o in outs:
+            o.fill_(1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = made(ws[(turn + 1) % 2], format, group, zero_points)
+        assert all(torch.equal(a, b) for a, b in zip(outs, wants[turn % 2])), turn
+        assert all(torch.equal(a, b) for a, b in zip(eager, wants[(turn + 1) % 2]))
